@@ -85,7 +85,7 @@ extern "C" {
 #define MXFP4_SCALES_ROWMAJOR 0 /* canonical: one byte per block, row-major */
 #define MXFP4_SCALES_MMA 1      /* GEMM-ready, see mxfp4_mma_scale_offset */
 
-/* Dequantize output type. */
+/* Dequantize output type; type of the int8 product and of dropout. */
 #define MXFP4_OUT_BF16 0
 #define MXFP4_OUT_F32 1
 
@@ -95,7 +95,9 @@ MXFP4_API const char *mxfp4_status_string(int status);
 /* ABI version (major * 100 + minor).  1.01 added mxfp4_gemm_bf16 and
  * mxfp4_grouped_gemm_bf16; 1.02 mxfp4_gemm_mxfp4; 1.03
  * mxfp4_grouped_gemm_wgrad_bf16; 1.04 mxfp4_scales_to_mma; 1.05
- * mxfp4_quantize_dual_rows. */
+ * mxfp4_quantize_dual_rows.  The expert feed-forward entry points
+ * (mxfp4_gated_*, mxfp4_int8_*, mxfp4_dropout) came after 1.05 and leave it
+ * unchanged: they add symbols and change none. */
 MXFP4_API int mxfp4_version(void);
 
 /*
@@ -429,6 +431,123 @@ MXFP4_API int mxfp4_nvfp4_dequantize(const uint8_t *codes, int64_t ld_codes, con
 MXFP4_API int mxfp4_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, const float *a_amax,
                                const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales, const float *b_amax,
                                int64_t M, int64_t N, int64_t K, float *c, int64_t ldc, void *stream);
+
+/*
+ * Gated feed-forward block ("Use in models / gpt-oss": the expert layer).  B
+ * holds the gate and the up projection in alternating rows (2j gate, 2j + 1
+ * up), as gpt-oss stores gate_up; z = A B^T is the pre-activation, and
+ *     g = min(z[2j], limit), u = clamp(z[2j + 1], -limit, limit)
+ *     h[j] = g * sigmoid(alpha g) * (u + beta)
+ * SwiGLU: alpha 1, limit INFINITY, beta 0; gpt-oss: alpha 1.702, limit 7, beta 1.
+ *
+ * mxfp4_gated_gemm, mxfp4_grouped_gated_gemm -- both projections, the
+ * activation and the product in one kernel: the operands of mxfp4_gemm /
+ * mxfp4_grouped_gemm (N = 2 x columns of h), h bf16 [M or a_rows, N/2] (row
+ * stride ldh elements).  The activation takes the FP32 accumulators; h is
+ * rounded once (nearest even).  z (optional, NULL = not kept): bf16 [.., N]
+ * (ldz), the accumulators rounded once, for the backward pass.  Rows outside
+ * the groups are left as they were.
+ *
+ * Requirements: as mxfp4_gemm / mxfp4_grouped_gemm; N even; h and z 16-byte
+ * aligned, ldh % 8 == 0, ldz % 8 == 0, not overlapping; alpha and beta finite,
+ * limit > 0.
+ */
+MXFP4_API int mxfp4_gated_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales,
+                               const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales,
+                               int64_t M, int64_t N, int64_t K, float alpha, float limit, float beta,
+                               uint16_t *h, int64_t ldh, uint16_t *z, int64_t ldz, void *stream);
+MXFP4_API int mxfp4_grouped_gated_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, int64_t a_rows,
+                                       const int32_t *group_offsets, const int32_t *group_sizes, int num_groups,
+                                       const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales,
+                                       int64_t N, int64_t K, float alpha, float limit, float beta,
+                                       uint16_t *h, int64_t ldh, uint16_t *z, int64_t ldz, void *stream);
+
+/*
+ * mxfp4_gated_gemm_backward, mxfp4_grouped_gated_gemm_backward -- the block's
+ * backward pass up to the pre-activations, in the epilogue of the down
+ * projection's data gradient: dh = A B^T (A = dY quantized along its columns,
+ * [M, K]; B = the down weight's transposed copy [N, K]; N = columns of h) is
+ * never stored, and with z as the forward pass kept it
+ *     s = sigmoid(alpha g)
+ *     dz[2j]     = dh[j] (u + beta) s (1 + alpha g (1 - s))   where z[2j] <= limit, else 0
+ *     dz[2j + 1] = dh[j] g s                                  where |z[2j + 1]| <= limit, else 0
+ * dz bf16 [M or a_rows, 2N] (lddz), rounded once; a NaN in z gives NaN.  dz
+ * may be z itself (same pointer and row stride); any other overlap is refused.
+ * The gradients of X and of the gate_up weight follow from dz by
+ * mxfp4_quantize_dual and the products of mxfp4_gemm and
+ * mxfp4_grouped_gemm_wgrad.  Requirements as for the forward form (N need not
+ * be even).
+ */
+MXFP4_API int mxfp4_gated_gemm_backward(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales,
+                                        const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales,
+                                        int64_t M, int64_t N, int64_t K, float alpha, float limit, float beta,
+                                        const uint16_t *z, int64_t ldz, uint16_t *dz, int64_t lddz, void *stream);
+MXFP4_API int mxfp4_grouped_gated_gemm_backward(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales,
+                                                int64_t a_rows, const int32_t *group_offsets,
+                                                const int32_t *group_sizes, int num_groups, const uint8_t *b_codes,
+                                                int64_t ldb, const uint8_t *b_scales, int64_t N, int64_t K,
+                                                float alpha, float limit, float beta, const uint16_t *z, int64_t ldz,
+                                                uint16_t *dz, int64_t lddz, void *stream);
+
+/*
+ * mxfp4_int8_quantize -- bf16 x[rows, cols] to signed 8-bit codes with one FP32
+ * scale per row (a token of activations, an output channel of a weight):
+ *     a = max(amax of the row, 2^-100), scales[row] = fp32(a / 127),
+ *     codes = nearest-even of fp32(x * fp32(127 / a)), within +-127.
+ * The value of a code is code * scale.  A NaN or Inf in a row gives it the
+ * scale NaN and codes 0.  codes [rows, cols] (ld_codes bytes), scales [rows].
+ * Requirements: rows, cols > 0; cols % 16 == 0; x and codes 16-byte aligned,
+ * ld_x % 8 == 0, ld_codes % 16 == 0.
+ */
+MXFP4_API int mxfp4_int8_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int8_t *codes,
+                                  int64_t ld_codes, float *scales, void *stream);
+
+/*
+ * mxfp4_int8_gemm -- C[M, N] = a_scales[m] * b_scales[n] * sum_k A[m, k] B[n, k]
+ * with signed 8-bit operands (tcgen05.mma kind::i8): the sum is exact in 32-bit
+ * integers, then FP32 (one rounding for the sum, one per factor), stored as
+ * FP32 or rounded once to bf16 (out_dtype MXFP4_OUT_F32 / MXFP4_OUT_BF16).
+ * Codes may be any of -128 .. 127.  A code that is 0 under the scale NaN gives
+ * NaN.  a_codes [M, K] (lda bytes), a_scales [M]; b_codes [N, K] (ldb), b_scales
+ * [N]; c [M, N] (ldc elements), fully overwritten.
+ *
+ * mxfp4_int8_grouped_gemm -- the same per group of rows, groups as in
+ * mxfp4_grouped_gemm; b_codes [num_groups, N, K], b_scales [num_groups, N];
+ * rows outside the groups are left as they were.
+ *
+ * Requirements: M, N >= 1; K >= 16, K % 16 == 0, K < 131072 (no sum leaves 32
+ * bits); codes and c 16-byte aligned; lda, ldb % 16 == 0; ldc * element size %
+ * 16 == 0.
+ */
+MXFP4_API int mxfp4_int8_gemm(const int8_t *a_codes, int64_t lda, const float *a_scales,
+                              const int8_t *b_codes, int64_t ldb, const float *b_scales,
+                              int64_t M, int64_t N, int64_t K, void *c, int64_t ldc, int out_dtype, void *stream);
+MXFP4_API int mxfp4_int8_grouped_gemm(const int8_t *a_codes, int64_t lda, const float *a_scales, int64_t a_rows,
+                                      const int32_t *group_offsets, const int32_t *group_sizes, int num_groups,
+                                      const int8_t *b_codes, int64_t ldb, const float *b_scales, int64_t N, int64_t K,
+                                      void *c, int64_t ldc, int out_dtype, void *stream);
+
+/*
+ * mxfp4_dropout -- y = [residual +] (kept ? x / (1 - p) : 0) for x[rows, cols],
+ * FP32 inside, rounded once.  Element (r, c), with g = r * cols + c +
+ * elem_offset, is kept iff word (g mod 4) of Philox4x32-10(key = seed, counter =
+ * (g/4, 0, 0x44524F50)) is at least round(p * 2^32): the indexing of
+ * mxfp4_quantize's stochastic rounding in a stream of its own, so a slice of
+ * rows with elem_offset = row0 * cols draws the whole tensor's mask.  The mask
+ * is never stored: the backward pass is the same call on dY with the same seed
+ * and elem_offset (no residual).  A dropped element is exactly 0 (or the
+ * residual) even where x is NaN or Inf.  p = 0 keeps and p = 1 drops all.
+ *
+ * dtype: MXFP4_OUT_BF16 or MXFP4_OUT_F32, of x, residual (NULL = none) and y.
+ * Any sizes, row strides (elements) and element alignment; 16-byte aligned
+ * pointers with rows of whole 16-byte pieces (or contiguous tensors) run
+ * fastest.  y may be x or residual itself (same pointer and row stride); any
+ * other overlap is refused.
+ * Requirements: rows, cols > 0; 0 <= p <= 1; elem_offset % 4 == 0.
+ */
+MXFP4_API int mxfp4_dropout(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,
+                            int64_t rows, int64_t cols, int dtype, double p, uint64_t seed, uint64_t elem_offset,
+                            void *y, int64_t ld_y, void *stream);
 
 /*
  * mxfp4_get_error -- synchronize `stream`, then return and clear the first

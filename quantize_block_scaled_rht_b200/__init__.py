@@ -46,6 +46,8 @@ ABI_FUNCTIONS = (
     "mxfp4_get_error",
     "mxfp4_set_wait_limit_ns", "mxfp4_wait_probe", "mxfp4_scales_to_mma",
     "mxfp4_quantize_dual_rows",
+    "mxfp4_gated_gemm", "mxfp4_grouped_gated_gemm", "mxfp4_gated_gemm_backward", "mxfp4_grouped_gated_gemm_backward",
+    "mxfp4_int8_quantize", "mxfp4_int8_gemm", "mxfp4_int8_grouped_gemm", "mxfp4_dropout",
 )
 
 
@@ -106,6 +108,21 @@ def lib() -> ctypes.CDLL:
         L.mxfp4_nvfp4_gemm.restype = i32
         L.mxfp4_scales_to_mma.argtypes = [vp, i64, i64, i64, i32, vp, vp]
         L.mxfp4_scales_to_mma.restype = i32
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        groups = [vp, vp, i32]
+        L.mxfp4_gated_gemm.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, f32, f32, f32, vp, i64, vp, i64, vp]
+        L.mxfp4_gated_gemm_backward.argtypes = L.mxfp4_gated_gemm.argtypes
+        L.mxfp4_grouped_gated_gemm.argtypes = [vp, i64, vp, i64, *groups, vp, i64, vp, i64, i64, f32, f32, f32,
+                                               vp, i64, vp, i64, vp]
+        L.mxfp4_grouped_gated_gemm_backward.argtypes = L.mxfp4_grouped_gated_gemm.argtypes
+        L.mxfp4_int8_quantize.argtypes = [vp, i64, i64, i64, vp, i64, vp, vp]
+        L.mxfp4_int8_gemm.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, i64, i32, vp]
+        L.mxfp4_int8_grouped_gemm.argtypes = [vp, i64, vp, i64, *groups, vp, i64, vp, i64, i64, vp, i64, i32, vp]
+        L.mxfp4_dropout.argtypes = [vp, i64, vp, i64, i64, i64, i32, f64, u64, u64, vp, i64, vp]
+        for name in ("mxfp4_gated_gemm", "mxfp4_gated_gemm_backward", "mxfp4_grouped_gated_gemm",
+                     "mxfp4_grouped_gated_gemm_backward", "mxfp4_int8_quantize", "mxfp4_int8_gemm",
+                     "mxfp4_int8_grouped_gemm", "mxfp4_dropout"):
+            getattr(L, name).restype = i32
         L.mxfp4_get_error.argtypes = [vp]
         L.mxfp4_get_error.restype = i32
         L.mxfp4_set_wait_limit_ns.argtypes = [u64]
@@ -523,6 +540,261 @@ def mxfp4_scales_to_mma(scales: torch.Tensor, rows: int, k: int, two_d: bool = F
     rc = lib().mxfp4_scales_to_mma(_ptr(scales), scales.stride(0), rows, k, 1 if two_d else 0, _ptr(out),
                                    _stream(stream))
     _check(rc, "mxfp4_scales_to_mma")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Expert feed-forward operators.  These take tensors of any CUDA device (the
+# call runs there, whatever the current device) and allocate their outputs on
+# the stream they run on.
+# ---------------------------------------------------------------------------
+
+def _call(fn, what: str, dev: torch.device, stream, *args) -> None:
+    """fn(*args, stream) with `dev` current; stream None = its current stream."""
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream))
+    if rc != MXFP4_OK:
+        raise MXFP4Error(rc, what)
+
+
+def _device(what: str, stream, *ts: Optional[torch.Tensor]) -> torch.device:
+    """The one CUDA device of the tensors (None skipped), checked against the stream's."""
+    dev = ts[0].device
+    if dev.type != "cuda":
+        raise ValueError("libmxfp4 takes CUDA tensors (device pointers)")
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{what}: tensors on different devices: {dev} and {t.device}")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"{what}: stream of {stream.device} for tensors on {dev}")
+    return dev
+
+
+def _empty(shape, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
+    """An output tensor that belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _empty_rows(rows: int, cols: int, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
+    """_empty whose rows start on 16-byte boundaries, as the kernels store them
+    (a view of a wider tensor where cols alone does not give that)."""
+    per = 16 // dtype.itemsize
+    if cols % per == 0:
+        return _empty((rows, cols), dtype, dev, stream)
+    return _empty((rows, (cols + per - 1) // per * per), dtype, dev, stream)[:, :cols]
+
+
+def _check_rows(t: torch.Tensor, what: str, dtype, shape) -> None:
+    """A 2-D row-major tensor (any row stride) of this type and shape."""
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape != shape or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a row-major tensor of shape {tuple(shape)}, got {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride; a single row's is never used and torch may leave any, so it
+    stands at a 16-byte multiple that covers the row."""
+    return (t.shape[1] + 15) // 16 * 16 if t.shape[0] == 1 else t.stride(0)
+
+
+def _check_groups(what: str, offsets: torch.Tensor, sizes: torch.Tensor, b: torch.Tensor) -> int:
+    if offsets.dtype != torch.int32 or sizes.dtype != torch.int32 or offsets.dim() != 1 or sizes.dim() != 1 or \
+            not offsets.is_contiguous() or not sizes.is_contiguous():
+        raise ValueError(f"{what}: group_offsets and group_sizes must be contiguous 1-D int32 tensors")
+    G = sizes.numel()
+    if offsets.numel() != G + 1:
+        raise ValueError(f"{what}: {G} group sizes need {G + 1} group offsets, got {offsets.numel()}")
+    if b.dim() != 3 or b.shape[0] != G or b.stride(2) != 1 or (G > 1 and b.stride(0) != b.shape[1] * b.stride(1)):
+        raise ValueError(f"{what}: B must be [{G}, N, K] with contiguous groups, got {tuple(b.shape)} with strides "
+                         f"{b.stride()}")
+    return G
+
+
+def _gated(name: str, a_codes, a_scales, groups, b_codes, b_scales, K, alpha, limit, beta, z, keep_z, out, stream):
+    """The four gated entry points: z None or a tensor to write (forward), or the
+    kept pre-activations (backward: keep_z is None)."""
+    grouped, backward = groups is not None, keep_z is None
+    if a_codes.dim() != 2 or a_codes.stride(1) != 1 or b_codes.dim() != (3 if grouped else 2) or b_codes.stride(-1) != 1:
+        raise ValueError(f"{name}: codes must be row-major, A [M, K/2] and B {'[G, N, K/2]' if grouped else '[N, K/2]'}")
+    M, N = a_codes.shape[0], b_codes.shape[-2]
+    G = _check_groups(name, *groups, b_codes) if grouped else 1
+    _check_operand(a_codes, a_scales, M, K, "A")
+    _check_operand(b_codes, b_scales, N, K, "B", groups=G)
+    if not a_scales.is_contiguous() or not b_scales.is_contiguous():
+        raise ValueError(f"{name}: scales must be contiguous")
+    if not backward and N % 2:
+        raise ValueError(f"{name}: B holds gate and up rows in turn, N = {N} is odd")
+    oshape, zshape = (M, 2 * N if backward else N // 2), (M, 2 * N if backward else N)
+    if z is not None:
+        _check_rows(z, "z", torch.bfloat16, zshape)
+    if out is not None:
+        _check_rows(out, "out", torch.bfloat16, oshape)
+    dev = _device(name, stream, a_codes, a_scales, b_codes, b_scales, z, out, *(groups or ()))
+    if out is None:
+        out = _empty_rows(*oshape, torch.bfloat16, dev, stream)
+    if keep_z and z is None:
+        z = _empty_rows(*zshape, torch.bfloat16, dev, stream)
+    first = (a_codes.data_ptr(), _ld(a_codes), a_scales.data_ptr())
+    second = (b_codes.data_ptr(), b_codes.stride(-2), b_scales.data_ptr())
+    rows = (M, groups[0].data_ptr(), groups[1].data_ptr(), G, *second, N, K) if grouped else (*second, M, N, K)
+    pz, po = (None if z is None else z.data_ptr(), 0 if z is None else _ld(z)), (out.data_ptr(), _ld(out))
+    _call(getattr(lib(), name), name, dev, stream, *first, *rows, alpha, limit, beta, *(pz + po if backward else po + pz))
+    return out, z
+
+
+def mxfp4_gated_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
+                     K: int, alpha: float = 1.0, limit: float = float("inf"), beta: float = 0.0, save_z: bool = False,
+                     out: Optional[torch.Tensor] = None, z_out: Optional[torch.Tensor] = None, stream=None):
+    """Gate and up projections, activation and product in one kernel: h =
+    g sigmoid(alpha g) (u + beta) of z = A B^T, gate and up in alternating rows
+    of B (see mxfp4_gated_gemm in include/mxfp4.h).  The defaults are SwiGLU.
+    Returns (h [M, N/2] bf16, z [M, N] bf16 or None); z, kept for the backward
+    pass, is written with save_z or a given z_out."""
+    return _gated("mxfp4_gated_gemm", a_codes, a_scales, None, b_codes, b_scales, K, alpha, limit, beta, z_out,
+                  bool(save_z), out, stream)
+
+
+def mxfp4_grouped_gated_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, group_offsets: torch.Tensor,
+                             group_sizes: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor, K: int,
+                             alpha: float = 1.0, limit: float = float("inf"), beta: float = 0.0, save_z: bool = False,
+                             out: Optional[torch.Tensor] = None, z_out: Optional[torch.Tensor] = None, stream=None):
+    """mxfp4_gated_gemm per expert: groups as in mxfp4_grouped_gemm, b_codes
+    [G, N, K/2].  Rows outside the groups are not written."""
+    return _gated("mxfp4_grouped_gated_gemm", a_codes, a_scales, (group_offsets, group_sizes), b_codes, b_scales, K,
+                  alpha, limit, beta, z_out, bool(save_z), out, stream)
+
+
+def mxfp4_gated_gemm_backward(dy_codes: torch.Tensor, dy_scales: torch.Tensor, wt_codes: torch.Tensor,
+                              wt_scales: torch.Tensor, z: torch.Tensor, K: int, alpha: float = 1.0,
+                              limit: float = float("inf"), beta: float = 0.0, out: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """dz [M, 2I] bf16 of the gated block: dh = dY Wdown (dY quantized row-wise
+    [M, K], the down weight's transposed copy [I, K]) through the derivative of
+    the activation at z (see mxfp4_gated_gemm_backward in include/mxfp4.h).
+    out may be z itself."""
+    return _gated("mxfp4_gated_gemm_backward", dy_codes, dy_scales, None, wt_codes, wt_scales, K, alpha, limit, beta, z,
+                  None, out, stream)[0]
+
+
+def mxfp4_grouped_gated_gemm_backward(dy_codes: torch.Tensor, dy_scales: torch.Tensor, group_offsets: torch.Tensor,
+                                      group_sizes: torch.Tensor, wt_codes: torch.Tensor, wt_scales: torch.Tensor,
+                                      z: torch.Tensor, K: int, alpha: float = 1.0, limit: float = float("inf"),
+                                      beta: float = 0.0, out: Optional[torch.Tensor] = None,
+                                      stream=None) -> torch.Tensor:
+    """mxfp4_gated_gemm_backward per expert: wt_codes [G, I, K/2].  Rows outside
+    the groups are not written."""
+    return _gated("mxfp4_grouped_gated_gemm_backward", dy_codes, dy_scales, (group_offsets, group_sizes), wt_codes,
+                  wt_scales, K, alpha, limit, beta, z, None, out, stream)[0]
+
+
+@dataclass
+class Int8Quantized:
+    """int8 codes [rows, cols] and one float32 scale per row."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def mxfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Quantized] = None, stream=None) -> Int8Quantized:
+    """Signed 8-bit codes and one scale per row of a 2-D bf16 tensor: activations
+    by token, a weight [N, K] by output channel (see mxfp4_int8_quantize in
+    include/mxfp4.h)."""
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D bfloat16 tensor")
+    _check_rows(x, "x", torch.bfloat16, x.shape)
+    rows, cols = x.shape
+    if out is not None:
+        _check_rows(out.codes, "out.codes", torch.int8, x.shape)
+        if out.scales.dtype != torch.float32 or out.scales.shape != (rows,) or not out.scales.is_contiguous():
+            raise ValueError(f"out.scales must be a contiguous float32 tensor of shape ({rows},)")
+    dev = _device("mxfp4_int8_quantize", stream, x, *((out.codes, out.scales) if out is not None else ()))
+    if out is None:
+        out = Int8Quantized(_empty((rows, cols), torch.int8, dev, stream), _empty((rows,), torch.float32, dev, stream))
+    _call(lib().mxfp4_int8_quantize, "mxfp4_int8_quantize", dev, stream, x.data_ptr(), rows, cols, _ld(x),
+          out.codes.data_ptr(), _ld(out.codes), out.scales.data_ptr())
+    return out
+
+
+def _int8_gemm(name: str, a_codes, a_scales, groups, b_codes, b_scales, out_dtype, out, stream) -> torch.Tensor:
+    grouped = groups is not None
+    if a_codes.dtype != torch.int8 or b_codes.dtype != torch.int8:
+        raise ValueError(f"{name}: codes must be int8 tensors")
+    if a_codes.dim() != 2 or a_codes.stride(1) != 1 or b_codes.dim() != (3 if grouped else 2) or b_codes.stride(-1) != 1:
+        raise ValueError(f"{name}: codes must be row-major, A [M, K] and B {'[G, N, K]' if grouped else '[N, K]'}")
+    M, K = a_codes.shape
+    N = b_codes.shape[-2]
+    if b_codes.shape[-1] != K:
+        raise ValueError(f"{name}: A has K = {K}, B {b_codes.shape[-1]}")
+    G = _check_groups(name, *groups, b_codes) if grouped else 1
+    for t, shape, what in ((a_scales, (M,), "a_scales"), (b_scales, (G, N) if grouped else (N,), "b_scales")):
+        if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: {what} must be a contiguous float32 tensor of shape {shape}, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+    if out is not None:
+        _check_rows(out, "out", (torch.bfloat16, torch.float32), (M, N))
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name}: out_dtype must be bfloat16 or float32")
+    dev = _device(name, stream, a_codes, a_scales, b_codes, b_scales, out, *(groups or ()))
+    if out is None:
+        out = _empty_rows(M, N, out_dtype, dev, stream)
+    first = (a_codes.data_ptr(), _ld(a_codes), a_scales.data_ptr())
+    second = (b_codes.data_ptr(), (K + 15) // 16 * 16 if N == 1 and not grouped else b_codes.stride(-2), b_scales.data_ptr())
+    rows = (M, groups[0].data_ptr(), groups[1].data_ptr(), G, *second, N, K) if grouped else (*second, M, N, K)
+    _call(getattr(lib(), name), name, dev, stream, *first, *rows, out.data_ptr(), _ld(out),
+          OUT_F32 if out_dtype == torch.float32 else OUT_BF16)
+    return out
+
+
+def mxfp4_int8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
+                    out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """C[M, N] = a_scales[m] b_scales[n] sum_k A[m, k] B[n, k] with int8 codes:
+    exact integer sums, token and channel scales in FP32 (see mxfp4_int8_gemm in
+    include/mxfp4.h).  Returns bfloat16 or float32."""
+    return _int8_gemm("mxfp4_int8_gemm", a_codes, a_scales, None, b_codes, b_scales, out_dtype, out, stream)
+
+
+def mxfp4_int8_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, group_offsets: torch.Tensor,
+                            group_sizes: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
+                            out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """mxfp4_int8_gemm per expert: groups as in mxfp4_grouped_gemm, b_codes
+    [G, N, K], b_scales [G, N].  Rows outside the groups are not written."""
+    return _int8_gemm("mxfp4_int8_grouped_gemm", a_codes, a_scales, (group_offsets, group_sizes), b_codes, b_scales,
+                      out_dtype, out, stream)
+
+
+def mxfp4_dropout(x: torch.Tensor, p: float, seed: int, elem_offset: int = 0, residual: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = [residual +] dropout(x) for a 2-D bf16 or fp32 tensor, the mask drawn
+    from the Philox stream of (seed, element index) and never stored (see
+    mxfp4_dropout in include/mxfp4.h).  The gradient is the same call on dY.
+    out may be x or residual itself."""
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D bfloat16 or float32 tensor")
+    _check_rows(x, "x", (torch.bfloat16, torch.float32), x.shape)
+    for t, what in ((residual, "residual"), (out, "out")):
+        if t is not None:
+            _check_rows(t, what, x.dtype, x.shape)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be within [0, 1], got {p}")
+    dev = _device("mxfp4_dropout", stream, x, residual, out)
+    if out is None:
+        out = _empty(x.shape, x.dtype, dev, stream)
+    res = (None, 0) if residual is None else (residual.data_ptr(), _ld(residual))
+    _call(lib().mxfp4_dropout, "mxfp4_dropout", dev, stream, x.data_ptr(), _ld(x), *res, x.shape[0], x.shape[1],
+          OUT_F32 if x.dtype == torch.float32 else OUT_BF16, p, seed & 0xFFFFFFFFFFFFFFFF, elem_offset, out.data_ptr(),
+          _ld(out))
     return out
 
 

@@ -1,12 +1,14 @@
 // api.cu -- the extern "C" boundary of libmxfp4 (declared in include/mxfp4.h):
 // argument validation, then one launch on the caller's stream.  No device
 // memory is allocated here; errors come back as status codes.
+#include <cmath>
 #include <cstdint>
 
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
 #include "common.cuh"
+#include "ffn.cuh"
 
 namespace mxfp4 {
 cudaError_t launch_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int layout, int rht,
@@ -422,6 +424,164 @@ int mxfp4_scales_to_mma(const uint8_t *scales, int64_t ld_scales, int64_t rows, 
     if (rows > (int64_t)1 << 40 || k > (int64_t)1 << 40) return MXFP4_ERR_UNSUPPORTED;
     const cudaError_t e = mxfp4::launch_scales_to_mma(scales, ld_scales, rows, k, two_d, mma_scales,
                                                       static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
+}
+
+// Gated forms: the activation's numbers, then the bf16 output(s).
+static bool valid_act(float alpha, float limit, float beta) {
+    return std::isfinite(alpha) && limit > 0.0f && std::isfinite(beta);   // limit may be infinite
+}
+
+// Row-major bf16 [rows, cols]: 16-byte rows.
+static int check_bf16(const void *p, int64_t ld, int64_t cols) {
+    if (!p || ld < cols) return MXFP4_ERR_INVALID_ARG;
+    return !aligned16(p) || (ld % 8) ? MXFP4_ERR_ALIGNMENT : MXFP4_OK;
+}
+
+static int gated_impl(const mxfp4::GatedArgs &a, void *stream) {
+    if (a.M <= 0 || a.N <= 0 || a.K <= 0 || !a.out) return MXFP4_ERR_INVALID_ARG;
+    if (!a.backward && (a.N % 2)) return MXFP4_ERR_INVALID_ARG;
+    if (!valid_act(a.alpha, a.limit, a.beta)) return MXFP4_ERR_INVALID_ARG;
+    // the FP32 output of check_gemm_common stands for no buffer here: N rounded
+    // up to 4 passes its leading-dimension checks
+    int rc = check_gemm_common(a.a_codes, a.lda, a.a_scales, a.b_codes, a.ldb, a.b_scales, a.N, a.K, a.out,
+                               (a.N + 3) / 4 * 4);
+    if (rc != MXFP4_OK) return rc;
+    rc = check_bf16(a.out, a.ld_out, a.backward ? 2 * a.N : a.N / 2);
+    if (rc != MXFP4_OK) return rc;
+    if (a.backward && !a.z) return MXFP4_ERR_INVALID_ARG;
+    const int64_t zcols = a.backward ? 2 * a.N : a.N;
+    if (a.z) {
+        rc = check_bf16(a.z, a.ldz, zcols);
+        if (rc != MXFP4_OK) return rc;
+    }
+    // z and the output: apart, or (backward) the same buffer with the same rows
+    if (a.z && !(a.backward && a.z == a.out && a.ldz == a.ld_out)) {
+        const char *z0 = static_cast<const char *>(a.z), *o0 = static_cast<const char *>(a.out);
+        const char *z1 = z0 + 2 * ((a.M - 1) * a.ldz + zcols);
+        const char *o1 = o0 + 2 * ((a.M - 1) * a.ld_out + (a.backward ? 2 * a.N : a.N / 2));
+        if (z0 < o1 && o0 < z1) return MXFP4_ERR_INVALID_ARG;
+    }
+    if (a.M > (int64_t)1 << 31 || a.N > (int64_t)1 << 30) return MXFP4_ERR_UNSUPPORTED;
+    return mxfp4::launch_gated(a, static_cast<cudaStream_t>(stream));
+}
+
+static int check_groups(const int32_t *group_offsets, const int32_t *group_sizes, int num_groups, int64_t N) {
+    if (!group_offsets || !group_sizes || num_groups <= 0 || N <= 0) return MXFP4_ERR_INVALID_ARG;
+    if (num_groups > 1024 || N > ((int64_t)1 << 31) / num_groups) return MXFP4_ERR_UNSUPPORTED;
+    return MXFP4_OK;
+}
+
+int mxfp4_gated_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, const uint8_t *b_codes, int64_t ldb,
+                     const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, float alpha, float limit, float beta,
+                     uint16_t *h, int64_t ldh, uint16_t *z, int64_t ldz, void *stream) {
+    Range range_("mxfp4_gated_gemm");
+    return gated_impl({a_codes, a_scales, b_codes, b_scales, lda, ldb, M, N, K, alpha, limit, beta, h, ldh, z, ldz,
+                       nullptr, nullptr, 1, false}, stream);
+}
+
+int mxfp4_grouped_gated_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, int64_t a_rows,
+                             const int32_t *group_offsets, const int32_t *group_sizes, int num_groups,
+                             const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales, int64_t N, int64_t K,
+                             float alpha, float limit, float beta, uint16_t *h, int64_t ldh, uint16_t *z, int64_t ldz,
+                             void *stream) {
+    Range range_("mxfp4_grouped_gated_gemm");
+    const int rc = check_groups(group_offsets, group_sizes, num_groups, N);
+    if (rc != MXFP4_OK) return rc;
+    return gated_impl({a_codes, a_scales, b_codes, b_scales, lda, ldb, a_rows, N, K, alpha, limit, beta, h, ldh, z, ldz,
+                       group_offsets, group_sizes, num_groups, false}, stream);
+}
+
+int mxfp4_gated_gemm_backward(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, const uint8_t *b_codes,
+                              int64_t ldb, const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, float alpha,
+                              float limit, float beta, const uint16_t *z, int64_t ldz, uint16_t *dz, int64_t lddz,
+                              void *stream) {
+    Range range_("mxfp4_gated_gemm_backward");
+    return gated_impl({a_codes, a_scales, b_codes, b_scales, lda, ldb, M, N, K, alpha, limit, beta, dz, lddz,
+                       const_cast<uint16_t *>(z), ldz, nullptr, nullptr, 1, true}, stream);
+}
+
+int mxfp4_grouped_gated_gemm_backward(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, int64_t a_rows,
+                                      const int32_t *group_offsets, const int32_t *group_sizes, int num_groups,
+                                      const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales, int64_t N,
+                                      int64_t K, float alpha, float limit, float beta, const uint16_t *z, int64_t ldz,
+                                      uint16_t *dz, int64_t lddz, void *stream) {
+    Range range_("mxfp4_grouped_gated_gemm_backward");
+    const int rc = check_groups(group_offsets, group_sizes, num_groups, N);
+    if (rc != MXFP4_OK) return rc;
+    return gated_impl({a_codes, a_scales, b_codes, b_scales, lda, ldb, a_rows, N, K, alpha, limit, beta, dz, lddz,
+                       const_cast<uint16_t *>(z), ldz, group_offsets, group_sizes, num_groups, true}, stream);
+}
+
+int mxfp4_int8_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int8_t *codes, int64_t ld_codes,
+                        float *scales, void *stream) {
+    Range range_("mxfp4_int8_quantize");
+    if (!x || !codes || !scales) return MXFP4_ERR_INVALID_ARG;
+    if (rows <= 0 || cols <= 0 || (cols % 16)) return MXFP4_ERR_INVALID_ARG;
+    if (ld_x < cols || ld_codes < cols) return MXFP4_ERR_INVALID_ARG;
+    if (!aligned16(x) || (ld_x % 8) || !aligned16(codes) || (ld_codes % 16) ||
+        (reinterpret_cast<uintptr_t>(scales) & 3u))
+        return MXFP4_ERR_ALIGNMENT;
+    if (rows >= (int64_t)1 << 31) return MXFP4_ERR_UNSUPPORTED;
+    const cudaError_t e = mxfp4::launch_int8_quantize(x, rows, cols, ld_x, codes, ld_codes, scales,
+                                                      static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
+}
+
+static int int8_gemm_impl(const mxfp4::Int8Args &a, int out_dtype, void *stream) {
+    if (!a.a || !a.b || !a.a_scales || !a.b_scales || !a.c) return MXFP4_ERR_INVALID_ARG;
+    if (a.M <= 0 || a.N <= 0 || a.K <= 0 || (a.K % 16)) return MXFP4_ERR_INVALID_ARG;
+    if (out_dtype != MXFP4_OUT_BF16 && out_dtype != MXFP4_OUT_F32) return MXFP4_ERR_INVALID_ARG;
+    if (a.lda < a.K || a.ldb < a.K || a.ldc < a.N) return MXFP4_ERR_INVALID_ARG;
+    if (!aligned16(a.a) || !aligned16(a.b) || !aligned16(a.c) || (a.lda % 16) || (a.ldb % 16) ||
+        ((a.ldc * (a.bf16 ? 2 : 4)) % 16) || (reinterpret_cast<uintptr_t>(a.a_scales) & 3u) ||
+        (reinterpret_cast<uintptr_t>(a.b_scales) & 3u))
+        return MXFP4_ERR_ALIGNMENT;
+    // sums of K products up to 2^14 must stay below 2^31
+    if (a.K >= 131072 || a.M > (int64_t)1 << 31 || a.N > (int64_t)1 << 31) return MXFP4_ERR_UNSUPPORTED;
+    return mxfp4::launch_int8_gemm(a, static_cast<cudaStream_t>(stream));
+}
+
+int mxfp4_int8_gemm(const int8_t *a_codes, int64_t lda, const float *a_scales, const int8_t *b_codes, int64_t ldb,
+                    const float *b_scales, int64_t M, int64_t N, int64_t K, void *c, int64_t ldc, int out_dtype,
+                    void *stream) {
+    Range range_("mxfp4_int8_gemm");
+    return int8_gemm_impl({a_codes, b_codes, a_scales, b_scales, lda, ldb, M, N, K, c, ldc, out_dtype == MXFP4_OUT_BF16,
+                           nullptr, nullptr, 1}, out_dtype, stream);
+}
+
+int mxfp4_int8_grouped_gemm(const int8_t *a_codes, int64_t lda, const float *a_scales, int64_t a_rows,
+                            const int32_t *group_offsets, const int32_t *group_sizes, int num_groups,
+                            const int8_t *b_codes, int64_t ldb, const float *b_scales, int64_t N, int64_t K, void *c,
+                            int64_t ldc, int out_dtype, void *stream) {
+    Range range_("mxfp4_int8_grouped_gemm");
+    const int rc = check_groups(group_offsets, group_sizes, num_groups, N);
+    if (rc != MXFP4_OK) return rc;
+    return int8_gemm_impl({a_codes, b_codes, a_scales, b_scales, lda, ldb, a_rows, N, K, c, ldc,
+                           out_dtype == MXFP4_OUT_BF16, group_offsets, group_sizes, num_groups}, out_dtype, stream);
+}
+
+int mxfp4_dropout(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, int64_t rows, int64_t cols,
+                  int dtype, double p, uint64_t seed, uint64_t elem_offset, void *y, int64_t ld_y, void *stream) {
+    Range range_("mxfp4_dropout");
+    if (!x || !y || rows <= 0 || cols <= 0) return MXFP4_ERR_INVALID_ARG;
+    if (dtype != MXFP4_OUT_BF16 && dtype != MXFP4_OUT_F32) return MXFP4_ERR_INVALID_ARG;
+    if (!(p >= 0.0 && p <= 1.0) || (elem_offset & 3u)) return MXFP4_ERR_INVALID_ARG;
+    if (rows > 1 && (ld_x < cols || ld_y < cols || (residual && ld_residual < cols))) return MXFP4_ERR_INVALID_ARG;
+    if (rows > ((int64_t)1 << 62) / cols) return MXFP4_ERR_UNSUPPORTED;
+    const uintptr_t size = dtype == MXFP4_OUT_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(x) % size || reinterpret_cast<uintptr_t>(y) % size ||
+        reinterpret_cast<uintptr_t>(residual) % size)
+        return MXFP4_ERR_ALIGNMENT;
+    // in place element for element (y over x or over the residual), or apart
+    const char *y0 = static_cast<const char *>(y), *y1 = y0 + size * ((rows - 1) * ld_y + cols);
+    auto bad = [&](const void *q, int64_t ld) {
+        const char *q0 = static_cast<const char *>(q), *q1 = q0 + size * ((rows - 1) * ld + cols);
+        return q && !(q0 == y0 && (rows == 1 || ld == ld_y)) && q0 < y1 && y0 < q1;
+    };
+    if (bad(x, ld_x) || bad(residual, ld_residual)) return MXFP4_ERR_INVALID_ARG;
+    const cudaError_t e = mxfp4::launch_dropout(x, ld_x, residual, ld_residual, rows, cols, dtype, p, seed, elem_offset,
+                                                y, ld_y, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
 }
 

@@ -36,6 +36,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "ffn.cuh"
 #include "ptx.cuh"
 
 namespace mxfp4 {
@@ -44,7 +45,6 @@ constexpr int BM = 128;                               // rows per CTA
 constexpr int CHUNK = 128;                            // K bytes per swizzled chunk (256 E2M1 = 8 scale blocks)
 constexpr int EPI_WARPS = 4;
 constexpr int EPI_BUF = 32 * 32 * 4;                  // 32 rows x 32 FP32
-constexpr int EPI_BYTES = EPI_WARPS * 2 * EPI_BUF;
 constexpr int BAR_BYTES = 256;
 constexpr int NUM_THREADS = 192;
 constexpr uint32_t TMEM_COLS = 512;
@@ -53,18 +53,26 @@ constexpr int MAX_STAGES = 8;
 
 // Tile configuration: a pair tile is 256 x BN; each stage of the STAGES-deep
 // smem ring holds KCH chunks of K (KCH * 256 E2M1 elements, 4 * KCH MMAs).
-// NV: NVFP4 operands (UE4M3 scales per 16 elements, kind::mxf4nvf4) instead of
-// MXFP4 (UE8M0 per 32, kind::mxf4).  A scale atom holds 4 blocks of every row
-// of a 128-row tile: 128 K-elements for MXFP4, 64 for NVFP4.
-template <int BN_, int STAGES_, int KCH_, bool NV_ = false>
+// KIND_NV: NVFP4 operands (UE4M3 scales per 16 elements, kind::mxf4nvf4) instead
+// of MXFP4 (UE8M0 per 32, kind::mxf4).  A scale atom holds 4 blocks of every row
+// of a 128-row tile: 128 K-elements for MXFP4, 64 for NVFP4.  KIND_I8: signed
+// 8-bit integers (kind::i8, exact 32-bit integer sums), one element per byte and
+// no scale atoms; the token and channel scales go in with the epilogue.
+// EPI_BUFS: 4 KB staging buffers per epilogue warp.
+constexpr int KIND_MX = 0, KIND_NV = 1, KIND_I8 = 2;
+template <int BN_, int STAGES_, int KCH_, int KIND_ = KIND_MX, int EPI_BUFS_ = 2>
 struct TileCfg {
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
     static constexpr int KCH = KCH_;
-    static constexpr bool NV = NV_;
-    static constexpr int KSTEP = 256 * KCH;           // E2M1 elements of K per stage
+    static constexpr bool NV = KIND_ == KIND_NV, I8 = KIND_ == KIND_I8;
+    static constexpr int EPI_BUFS = EPI_BUFS_;
+    static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * EPI_BUF;
+    static constexpr int KPB = I8 ? 1 : 2;            // K-elements per byte
+    static constexpr int KMMA = 32 * KPB;             // K-elements per instruction (32 bytes)
+    static constexpr int KSTEP = 128 * KPB * KCH;     // K-elements per stage
     static constexpr int KATOM = NV ? 64 : 128;       // K-elements per scale atom
-    static constexpr int NATOM = KSTEP / KATOM;       // scale atoms per row tile per stage
+    static constexpr int NATOM = I8 ? 0 : KSTEP / KATOM;   // scale atoms per row tile per stage
     // B scale atoms span one 128-row tile when BN = 128, two when BN = 192
     // (a 192-column tile starts at 0 or 64 within a 128-row scale tile).
     static constexpr int NRT = BN == 128 ? 1 : 2;
@@ -76,7 +84,7 @@ struct TileCfg {
     static constexpr int SFB_BYTES = NRT * NATOM * 512;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
     static constexpr uint32_t STAGE_TX = 2u * STAGE_BYTES;   // both CTAs complete on the even CTA's barrier
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES + 1024;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES + 1024;   // + alignment
     // TMEM columns (per CTA): accumulator 0 at [0, BN), the scale factors of
     // two consecutive stages after it, accumulator 1 at the top.
     static constexpr uint32_t SF_COL = BN;
@@ -85,9 +93,10 @@ struct TileCfg {
     // Instruction descriptor, kind::mxf4 block-scaled: A/B E2M1 (1), K-major,
     // N >> 3 at bit 17, UE8M0 scales (bit 23), M >> 4 at bit 24 (M = 256 for
     // the pair), scale-factor byte selectors at bits 4 (B) and 29 (A).
+    // kind::i8: signed A and B (1), 32-bit integer accumulators (2 at bit 4).
     static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
-                                      ((NV ? 0u : 1u) << 23) | ((uint32_t)(256 >> 4) << 24);
-    static_assert(BN == 128 || BN == 192, "tile width");
+                                      (I8 ? 2u << 4 : (NV ? 0u : 1u) << 23) | ((uint32_t)(256 >> 4) << 24);
+    static_assert(BN == 128 || BN == 192 || (I8 && (BN == 64 || BN == 256)), "tile width");
     static_assert(KCH == 1 || KCH == 2, "chunks per stage");
     static_assert(STAGES <= MAX_STAGES, "stages");
     static_assert(SF_COL + 2 * SF_STAGE_COLS <= ACC1_COL, "TMEM layout");
@@ -97,10 +106,24 @@ struct TileCfg {
 
 // Output of the epilogue: FP32, bf16 (nearest even), or MXFP4 (each 1D row
 // block of 32 FP32 results requantized: amax, E8M0 scale, E2M1 RNE codes).
-constexpr int OUT_F32 = 0, OUT_BF16 = 1, OUT_MX = 2;
+// OUT_GATED: the gated activation of column pairs (2j gate, 2j + 1 up) to bf16 h
+// [.., N/2], with the pre-activations z optionally kept in bf16.  OUT_GATED_BWD:
+// the accumulators are dh; with z they give dz (bf16 [.., 2N]).
+constexpr int OUT_F32 = 0, OUT_BF16 = 1, OUT_MX = 2, OUT_GATED = 3, OUT_GATED_BWD = 4;
 
 using DefaultCfg = TileCfg<192, 3, 2>;
-using NvCfg = TileCfg<192, 5, 1, true>;
+using NvCfg = TileCfg<192, 5, 1, KIND_NV>;
+// The backward pass streams z in and dz out through the same staging buffers:
+// four per warp keep two loads ahead of the box being computed, paid for with a
+// ring of 5 x 256 instead of 3 x 512 K-elements.
+using BwdCfg = TileCfg<192, 5, 1, KIND_MX, 4>;
+// int8: twice the operand bytes per K of MXFP4 at half the MMA rate, so L2
+// traffic per MMA cycle is the same; without scale factors in tensor memory two
+// 256-column accumulators fit, and a 256 x 256 tile reads 1/8 fewer operand
+// bytes per product than 256 x 192.
+using I8Cfg = TileCfg<256, 3, 2, KIND_I8>;
+using I8GroupedCfg = TileCfg<256, 5, 1, KIND_I8>;   // the group table takes 4 KB of shared memory
+using I8NarrowCfg = TileCfg<64, 6, 1, KIND_I8>;
 
 __device__ unsigned int g_error_code;
 
@@ -118,6 +141,10 @@ struct GemmParams {
     const int32_t *group_offsets;
     const int32_t *group_sizes;
     const float *a_amax, *b_amax;   // NVFP4 tensor amaxes (second-level scales amax / 2688)
+    const float *a_tok, *b_chan;    // int8: one scale per row of A, one per row of B (all groups')
+    void *z;                        // gated: pre-activations out (may be null); backward: in
+    int64_t ldz;
+    float act_alpha, act_limit, act_beta;
     int num_groups;
     uint64_t wait_limit_ns;
 };
@@ -234,6 +261,126 @@ __device__ __forceinline__ TileInfo get_tile(int t, uint32_t rank, const GemmPar
     return ti;
 }
 
+// int8 epilogue: 32 integer sums of one row to (sum * token scale) * channel
+// scale.  A sum up to 2^31 is rounded once to FP32 (24 bits) and each factor
+// once: three half-steps of 2^-24, far below bf16's and within 2e-7 for FP32.
+// Lane i holds the channel scale of column i of the step.
+__device__ __forceinline__ void scale_i8(uint32_t *v, float tok, float chan) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float c = __shfl_sync(0xFFFFFFFFu, chan, i);
+        v[i] = __float_as_uint(__fmul_rn(__fmul_rn(__int2float_rn((int)v[i]), tok), c));
+    }
+}
+
+// 64-byte swizzled staging row (32 bf16) and 128-byte one (64 bf16): the
+// 16-byte unit index is xored with address bits 7-8 or 7-9, as the tensor maps
+// of the stores expect, which also spreads a warp's rows over all banks.
+__device__ __forceinline__ void stage_row64(uint32_t buf, int lane, const uint32_t *w) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + (uint32_t)lane * 64u +
+                                                                      (((uint32_t)c ^ ((lane >> 1) & 3)) << 4)),
+                     "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                     : "memory");
+}
+__device__ __forceinline__ void stage_row128(uint32_t buf, int lane, const uint32_t *w) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(buf + (uint32_t)lane * 128u +
+                                                                      (((uint32_t)c ^ (lane & 7)) << 4)),
+                     "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                     : "memory");
+}
+__device__ __forceinline__ void unstage_row128(uint32_t buf, int lane, uint32_t *w) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                     : "r"(buf + (uint32_t)lane * 128u + (((uint32_t)c ^ (lane & 7)) << 4))
+                     : "memory");
+}
+
+// 8 * NV bf16 of one row straight to or from global memory, columns at or past
+// `left` untouched (16-byte pieces; the rows are 16-byte aligned).
+template <int NV>
+__device__ __forceinline__ void store_row_bf16(uint16_t *dst, const uint32_t *w, int64_t left) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        if (8 * c + 8 <= left) {
+            asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(dst + 8 * c), "r"(w[4 * c]),
+                         "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                         : "memory");
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (8 * c + e < left) dst[8 * c + e] = (uint16_t)(w[4 * c + e / 2] >> (16 * (e & 1)));
+        }
+    }
+}
+template <int NV>
+__device__ __forceinline__ void load_row_bf16(const uint16_t *src, uint32_t *w, int64_t left) {
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        if (8 * c + 8 <= left) {
+            asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                         : "l"(src + 8 * c)
+                         : "memory");
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const uint32_t lo = 8 * c + e < left ? src[8 * c + e] : 0, hi = 8 * c + e + 1 < left ? src[8 * c + e + 1] : 0;
+                w[4 * c + e / 2] = lo | (hi << 16);
+            }
+        }
+    }
+}
+
+// A tensor-map store whose box reaches past the last column still writes whole
+// 16-byte units: where the columns do not end on one (ncols elements of `esize`
+// bytes) it would put zeros into the columns behind them, which belong to the
+// caller, so the box of `width` columns at `col` goes out with plain stores.
+__device__ __forceinline__ bool ragged_box(int64_t col, int width, int64_t ncols, int esize) {
+    return col + width > ncols && (ncols * esize) % 16 != 0;
+}
+
+// Backward epilogue, per warp: z boxes (32 rows x 64 columns, 4 KB) stream into
+// a ring of staging buffers by TMA, two boxes ahead of the one computed; each
+// box is replaced in place by dz and stored.  Buffer n % EPI_BUFS takes load n
+// once the store of load n - EPI_BUFS has read it: with two ahead, of the
+// stores committed so far all but the newest must have been read.  Boxes that
+// reach past their group's rows, and ragged ones, do not go through the ring.
+template <class Cfg, int MODE>
+struct ZRing {
+    int t, j;                // next box to look at: pair tile, 32-column step
+    uint32_t issued, used;
+    TileInfo ti;
+
+    __device__ __forceinline__ void start(int t0) { t = t0; j = 0; issued = used = 0; }
+    // Issue loads until two boxes past the current one are in flight.
+    __device__ __forceinline__ void fill(const CUtensorMap *map, uint8_t *bufs, uint64_t *bars, const GemmParams &p,
+                                         const int *cum, int tiles_n, int ntiles, int npairs, uint32_t rank,
+                                         int row_lo, int lane) {
+        while (issued < used + 3 && t < ntiles) {
+            if (j == 0) ti = get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n);
+            const bool boxes = row_lo < ti.rows_valid && (MODE == MODE_DENSE || row_lo + 32 <= ti.rows_valid);
+            const int64_t col0 = ti.n0 + 32 * j;
+            if (boxes && col0 < p.N && !ragged_box(2 * col0, 64, 2 * p.N, 2)) {
+                if (lane == 0) {
+                    const uint32_t b = issued % Cfg::EPI_BUFS;
+                    if (issued >= Cfg::EPI_BUFS) bulk_wait_group_read<1>();
+                    mbar_arrive_expect_tx(&bars[b], EPI_BUF);
+                    tma_load_2d(bufs + b * EPI_BUF, map, (int32_t)(2 * col0), (int32_t)(ti.c_row0 + row_lo), &bars[b]);
+                }
+                ++issued;
+            }
+            if (!boxes || ++j == Cfg::BN / 32) { j = 0; t += npairs; }
+        }
+        __syncwarp();
+    }
+};
+
 // One K stage of the pair tile, issued by the converged MMA warp: the stage's
 // scale atoms go to tensor memory (A: NATOMS atoms of this pair's rows; B: NRT
 // 128-row tiles x NATOMS atoms), then NK MMAs of K = 64 walk the 128-byte
@@ -244,6 +391,17 @@ template <class Cfg, int NATOMS, int NK>
 __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint32_t st, uint32_t sfa_col, uint32_t b_shift,
                                             bool first) {
     constexpr int NRT = Cfg::NRT, NATOM = Cfg::NATOM;
+    if constexpr (Cfg::I8) {
+        const uint64_t adesc = smem_desc(st, 16, 1024, 2);
+        const uint64_t bdesc = smem_desc(st + Cfg::A_BYTES, 16, 1024, 2);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            const uint64_t a_off = (uint64_t)(((k >> 2) * Cfg::A_CHUNK + (k & 3) * 32) >> 4);
+            const uint64_t b_off = (uint64_t)(((k >> 2) * Cfg::B_CHUNK + (k & 3) * 32) >> 4);
+            mma_i8_pair_elect(d_tmem, adesc + a_off, bdesc + b_off, Cfg::IDESC, (k == 0 && first) ? 0u : 1u);
+        }
+        return;
+    }
     const uint32_t sfb_col = sfa_col + 4u * NATOM;
     const uint64_t sf_desc = smem_desc(st + Cfg::A_BYTES + Cfg::B_BYTES, 0, 128, 0);
 #pragma unroll
@@ -272,8 +430,8 @@ __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint32_t st, uint32
     }
 }
 
-// Partial last K stage (K not a multiple of the stage depth): NK = kleft / 64
-// MMAs and ceil(NK / 2) scale atoms.
+// Partial last K stage (K not a multiple of the stage depth): NK = ceil(kleft /
+// KMMA) MMAs (kleft / 64 for E2M1) and ceil(NK / 2) scale atoms.
 template <class Cfg>
 __device__ __noinline__ void issue_stage_tail(uint32_t d_tmem, uint32_t st, uint32_t sfa_col, uint32_t b_shift,
                                               bool first, int nk) {
@@ -302,7 +460,8 @@ template <class Cfg, int MODE, int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
                       const __grid_constant__ CUtensorMap tma_c, const __grid_constant__ CUtensorMap tma_sfa,
-                      const __grid_constant__ CUtensorMap tma_sfb, const GemmParams p) {
+                      const __grid_constant__ CUtensorMap tma_sfb, const __grid_constant__ CUtensorMap tma_z,
+                      const GemmParams p) {
     constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES;
     constexpr int A_BYTES = Cfg::A_BYTES, B_BYTES = Cfg::B_BYTES, SFA_BYTES = Cfg::SFA_BYTES;
     constexpr int STAGE_BYTES = Cfg::STAGE_BYTES, KCH = Cfg::KCH, NATOM = Cfg::NATOM;
@@ -310,9 +469,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *stage_base = smem;
     uint8_t *epi_base = smem + STAGES * STAGE_BYTES;
-    Shared *sh = reinterpret_cast<Shared *>(epi_base + EPI_BYTES);
+    Shared *sh = reinterpret_cast<Shared *>(epi_base + Cfg::EPI_BYTES);
     constexpr bool GROUPED = MODE == MODE_GROUPED_M;
     __shared__ int cum[MODE != MODE_DENSE ? MAX_GROUPS + 1 : 1];
+    __shared__ uint64_t zbar[OUT == OUT_GATED_BWD ? EPI_WARPS * Cfg::EPI_BUFS : 1];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();               // 0 = MMA issuer of the pair
@@ -325,6 +485,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         for (int s = 0; s < STAGES; ++s) { mbar_init(&sh->full[s], 1); mbar_init(&sh->empty[s], 1); }
         for (int b = 0; b < 2; ++b) { mbar_init(&sh->tmem_full[b], 1); mbar_init(&sh->tmem_empty[b], 2 * EPI_WARPS); }
         mbar_init(&sh->drain, 1);
+        if constexpr (OUT == OUT_GATED_BWD)
+            for (int b = 0; b < EPI_WARPS * Cfg::EPI_BUFS; ++b) mbar_init(&zbar[b], 1);
         sh->abort = 0;
         sh->drain_failed = 0;
         fence_barrier_init();
@@ -332,8 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         prefetch_tmap(&tma_a);
         prefetch_tmap(&tma_b);
         prefetch_tmap(&tma_c);
-        prefetch_tmap(&tma_sfa);
-        prefetch_tmap(&tma_sfb);
+        if constexpr (!Cfg::I8) {
+            prefetch_tmap(&tma_sfa);
+            prefetch_tmap(&tma_sfb);
+        }
+        if constexpr (OUT == OUT_GATED || OUT == OUT_GATED_BWD) prefetch_tmap(&tma_z);
     }
     if (warp == 1) {
         tmem_alloc_pair(&sh->tmem_base, TMEM_COLS);
@@ -414,16 +579,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                         if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], Cfg::STAGE_TX);
 #pragma unroll
                         for (int c = 0; c < KCH; ++c) {
-                            const int32_t kx = (int32_t)(ti.k0 / 2) + (kt * KCH + c) * CHUNK;
+                            const int32_t kx = (int32_t)(ti.k0 / Cfg::KPB) + (kt * KCH + c) * CHUNK;
                             tma_load_2d_pair(st + c * Cfg::A_CHUNK, &tma_a, kx, (int32_t)ti.row0, full_leader);
                             tma_load_2d_pair(st + A_BYTES + c * Cfg::B_CHUNK, &tma_b, kx,
                                              (int32_t)(ti.b_row + rank * (BN / 2)), full_leader);
                         }
                         // scale atoms: NATOM consecutive K atoms of one (A) or NRT (B) 128-row tiles
-                        tma_load_3d_pair(st + A_BYTES + B_BYTES, &tma_sfa, 0, katom0 + kt * NATOM, sfa_rt,
-                                         full_leader);
-                        tma_load_3d_pair(st + A_BYTES + B_BYTES + SFA_BYTES, &tma_sfb, 0, katom0 + kt * NATOM,
-                                         sfb_rt, full_leader);
+                        if constexpr (!Cfg::I8) {
+                            tma_load_3d_pair(st + A_BYTES + B_BYTES, &tma_sfa, 0, katom0 + kt * NATOM, sfa_rt,
+                                             full_leader);
+                            tma_load_3d_pair(st + A_BYTES + B_BYTES + SFA_BYTES, &tma_sfb, 0, katom0 + kt * NATOM,
+                                             sfb_rt, full_leader);
+                        }
                     }
                     __syncwarp();
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -465,10 +632,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     const int64_t kleft = ti.kg - (int64_t)kt * Cfg::KSTEP;
                     const uint32_t sfa_col = tmem + Cfg::SF_COL + Cfg::SF_STAGE_COLS * (kglobal & 1u);
                     const uint32_t st = smem_u32(stage_base + s * STAGE_BYTES);
-                    if (kleft >= Cfg::KSTEP)
+                    // a stage whose last instruction is partial (int8, K not a
+                    // multiple of 32) is full too: TMA filled it up with zeros
+                    if (kleft > Cfg::KSTEP - Cfg::KMMA)
                         issue_stage<Cfg, NATOM, 4 * KCH>(d_tmem, st, sfa_col, b_shift, kt == 0);
                     else
-                        issue_stage_tail<Cfg>(d_tmem, st, sfa_col, b_shift, kt == 0, (int)(kleft / 64));
+                        issue_stage_tail<Cfg>(d_tmem, st, sfa_col, b_shift, kt == 0,
+                                              (int)((kleft + Cfg::KMMA - 1) / Cfg::KMMA));
                     issued = true;
                     tc_commit_pair_elect(&sh->empty[s]);
                     ++kglobal;
@@ -497,11 +667,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         // NVFP4: the product of the two second-level scales (amax / 2688 each)
         float nv_scale = 1.0f;
         if constexpr (Cfg::NV) nv_scale = __fmul_rn(__fdiv_rn(*p.a_amax, 2688.0f), __fdiv_rn(*p.b_amax, 2688.0f));
+        ZRing<Cfg, MODE> ring;
+        uint8_t *ring_bufs = epi_base + ew * Cfg::EPI_BUFS * EPI_BUF;
+        uint64_t *ring_bars = zbar + (OUT == OUT_GATED_BWD ? ew * Cfg::EPI_BUFS : 0);
+        ring.start(pair);
         for (int t = pair; t < ntiles; t += npairs) {
             const TileInfo ti = get_tile<BN, MODE>(t, rank, p, cum, tiles_n);
+            const int row_lo = 32 * q;
+            // int8: this lane's token scale, and the channel scale of column
+            // 32 j + lane of the tile, one 32-column step ahead
+            auto load_chan = [&](int j) {
+                const int64_t col = ti.n0 + 32 * j + lane;
+                return j < BN / 32 && col < p.N ? __ldg(p.b_chan + (ti.b_row - ti.n0) + col) : 0.0f;
+            };
+            float tok = 0.0f, chan = 0.0f;
+            if constexpr (Cfg::I8) {
+                if (row_lo + lane < ti.rows_valid) tok = __ldg(p.a_tok + ti.c_row0 + row_lo + lane);
+                chan = load_chan(0);
+            }
+            if constexpr (OUT == OUT_GATED_BWD)
+                ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane);
             if (!wait_phase(&sh->tmem_full[acc], acc_ph, sh, limit)) break;
             tc_fence_after();
-            const int row_lo = 32 * q;
             const bool full_box = MODE == MODE_DENSE || (row_lo + 32 <= ti.rows_valid);
             const bool any_row = row_lo < ti.rows_valid;
             const bool empty_k = ti.kg <= 0;              // grouped K: an empty group's output is zero
@@ -549,6 +736,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     if (p.c_scale_mma) p.c_scales[mma_scale_off(row, kb, p.c_katoms)] = (uint8_t)code;
                     else p.c_scales[row * p.ld_c_scales + kb] = (uint8_t)code;
                 }
+            } else if constexpr (OUT == OUT_GATED) {
+                // 64 columns of z per step: a lane holds 32 (gate, up) pairs of
+                // one row, so the activation needs no exchange between lanes;
+                // 32 h (and the 64 z, if kept) leave as one box each
+                const GatedAct act{p.act_alpha, p.act_limit, p.act_beta};
+                const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16) + (acc ? Cfg::ACC1_COL : 0u);
+                for (int j = 0; j < BN / 64; ++j) {
+                    uint32_t w[32], hw[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(tm + 64u * j + 32u * h, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            hw[8 * h + i] = pack_bf16x2(
+                                act.forward(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+                                act.forward(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[16 * h + i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    }
+                    if (j == BN / 64 - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
+                    }
+                    const int64_t col0 = ti.n0 + 64 * j;
+                    if (!any_row || col0 >= p.N) continue;
+                    if (full_box && !ragged_box(col0 >> 1, 32, p.N >> 1, 2)) {
+                        for (int o = p.z ? 0 : 1; o < 2; ++o) {
+                            uint8_t *buf = epi_base + (ew * Cfg::EPI_BUFS + (buf_i & 1u)) * EPI_BUF;
+                            if (lane == 0) bulk_wait_group_read<1>();
+                            __syncwarp();
+                            if (o == 0) stage_row128(smem_u32(buf), lane, w);
+                            else stage_row64(smem_u32(buf), lane, hw);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (o == 0) tma_store_2d(&tma_z, (int32_t)col0, (int32_t)(ti.c_row0 + row_lo), buf);
+                                else tma_store_2d(&tma_c, (int32_t)(col0 >> 1), (int32_t)(ti.c_row0 + row_lo), buf);
+                                bulk_commit_group();
+                            }
+                            ++buf_i;
+                        }
+                    } else if (row_lo + lane < ti.rows_valid) {
+                        const int64_t row = ti.c_row0 + row_lo + lane;
+                        store_row_bf16<4>(static_cast<uint16_t *>(p.c) + row * p.ldc + (col0 >> 1), hw, (p.N - col0) >> 1);
+                        if (p.z) store_row_bf16<8>(static_cast<uint16_t *>(p.z) + row * p.ldz + col0, w, p.N - col0);
+                    }
+                }
+            } else if constexpr (OUT == OUT_GATED_BWD) {
+                // 32 columns of dh per step with the 64 columns of z they belong to
+                const GatedAct act{p.act_alpha, p.act_limit, p.act_beta};
+                const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16) + (acc ? Cfg::ACC1_COL : 0u);
+                bool ok = true;
+                for (int j = 0; j < BN / 32 && ok; ++j) {
+                    uint32_t v[32], w[32];
+                    tmem_ld_32x32b_x32(tm + 32u * j, v);
+                    tmem_ld_wait();
+                    if (j == BN / 32 - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
+                    }
+                    const int64_t col0 = ti.n0 + 32 * j;
+                    if (!any_row || col0 >= p.N) continue;
+                    const int64_t row = ti.c_row0 + row_lo + lane, zleft = 2 * (p.N - col0);
+                    const bool lane_row = row_lo + lane < ti.rows_valid;
+                    const bool in_ring = full_box && !ragged_box(2 * col0, 64, 2 * p.N, 2);
+                    const uint32_t b = ring.used % Cfg::EPI_BUFS;
+                    uint8_t *buf = ring_bufs + b * EPI_BUF;
+                    if (in_ring) {
+                        ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane);
+                        if (!wait_phase(&ring_bars[b], (ring.used / Cfg::EPI_BUFS) & 1u, sh, limit)) { ok = false; break; }
+                        unstage_row128(smem_u32(buf), lane, w);
+                    } else if (lane_row) {
+                        load_row_bf16<8>(static_cast<const uint16_t *>(p.z) + row * p.ldz + 2 * col0, w, zleft);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) w[i] = act.backward(__uint_as_float(v[i]), w[i]);
+                    if (in_ring) {
+                        stage_row128(smem_u32(buf), lane, w);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tma_c, (int32_t)(2 * col0), (int32_t)(ti.c_row0 + row_lo), buf);
+                            bulk_commit_group();
+                        }
+                        ++ring.used;
+                    } else if (lane_row) {
+                        store_row_bf16<8>(static_cast<uint16_t *>(p.c) + row * p.ldc + 2 * col0, w, zleft);
+                    }
+                }
+                if (!ok) break;
             } else if constexpr (OUT == OUT_BF16) {
                 // 64 columns per step: two 32-column TMEM loads rounded to
                 // bf16 pairs (RNE), one 128-byte row segment per lane
@@ -569,6 +854,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                             for (int i = 0; i < 32; ++i)
                                 v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), nv_scale));
                         }
+                        if constexpr (Cfg::I8) scale_i8(v, tok, chan);
+                        if constexpr (Cfg::I8) chan = load_chan(2 * j + h + 1);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             w[16 * h + i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
@@ -581,8 +868,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     if (!any_row) continue;
                     const int64_t col0 = ti.n0 + 64 * j;
                     if (col0 >= p.N) continue;
-                    if (full_box) {
-                        uint8_t *buf = epi_base + (ew * 2 + (buf_i & 1u)) * EPI_BUF;
+                    if (full_box && !(Cfg::I8 && ragged_box(col0, 64, p.N, 2))) {
+                        uint8_t *buf = epi_base + (ew * Cfg::EPI_BUFS + (buf_i & 1u)) * EPI_BUF;
                         if (lane == 0) bulk_wait_group_read<1>();
                         __syncwarp();
 #pragma unroll
@@ -628,6 +915,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), nv_scale));
                     }
+                    if constexpr (Cfg::I8) scale_i8(v, tok, chan);
+                    if constexpr (Cfg::I8) chan = load_chan(j + 1);
                     if (j == BN / 32 - 1) {
                         tc_fence_before();
                         __syncwarp();
@@ -636,8 +925,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     if (!any_row) continue;
                     const int64_t col0 = ti.n0 + 32 * j;
                     if (col0 >= p.N) continue;
-                    if (full_box) {
-                        uint8_t *buf = epi_base + (ew * 2 + (buf_i & 1u)) * EPI_BUF;
+                    if (full_box && !(Cfg::I8 && ragged_box(col0, 32, p.N, 4))) {
+                        uint8_t *buf = epi_base + (ew * Cfg::EPI_BUFS + (buf_i & 1u)) * EPI_BUF;
                         if (lane == 0) bulk_wait_group_read<1>();
                         __syncwarp();
     #pragma unroll
@@ -672,6 +961,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+        }
+        if constexpr (OUT == OUT_GATED_BWD) {
+            // after an abort: loads in flight land before the shared memory goes away
+            bool landed = true;
+            for (; ring.used < ring.issued; ++ring.used)
+                landed &= wait_phase(&ring_bars[ring.used % Cfg::EPI_BUFS], (ring.used / Cfg::EPI_BUFS) & 1u, sh, limit,
+                                     true);
+            if (!landed && lane == 0) mark_drain_failed(sh, rank);
         }
         if (lane == 0) bulk_wait_group_all();
         __syncwarp();
@@ -788,6 +1085,10 @@ struct GemmArgs {
     uint8_t *c_scales = nullptr;
     int64_t ld_c_scales = 0;
     int c_scale_mma = 0;
+    const float *a_tok = nullptr, *b_chan = nullptr;
+    void *z = nullptr;
+    int64_t ldz = 0;
+    float alpha = 1.0f, limit = 0.0f, beta = 0.0f;
 };
 
 // Returns 0 on success, MXFP4_ERR_CUDA when a map or launch fails.
@@ -795,7 +1096,9 @@ struct GemmArgs {
 // [G * M, N]; the B operand and C map cover G groups only in grouped-rows mode.
 // OUT_BF16: C is bf16 (RNE of the FP32 accumulators), stored in 64-column
 // boxes; OUT_MX: C is MXFP4 codes + scales written without the C tensor map
-// (a map over the codes is still passed, never used).
+// (a map over the codes is still passed, never used).  OUT_GATED: C is h
+// [.., N/2] in 32-column boxes and z [.., N], if kept, in 64-column ones;
+// OUT_GATED_BWD: z in and C = dz out, both [.., 2N], in 64-column boxes.
 template <class Cfg, int MODE, int OUT = OUT_F32>
 static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     constexpr int BN = Cfg::BN;
@@ -803,22 +1106,36 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     const int64_t c_rows = MODE == MODE_GROUPED_K ? (int64_t)g.G * g.M : g.M;
     const int64_t katoms = (g.K + Cfg::KATOM - 1) / Cfg::KATOM;
     const int64_t a_tiles = (g.M + 127) / 128, b_tiles = (g.N + 127) / 128;
-    CUtensorMap ta, tb, tc, tsa, tsb;
-    if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a_codes, (uint64_t)(g.K / 2), (uint64_t)g.M,
-                  (uint64_t)g.lda, CHUNK, BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b_codes, (uint64_t)(g.K / 2), (uint64_t)G * g.N,
-                  (uint64_t)g.ldb, CHUNK, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !(OUT == OUT_MX
-              ? make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.c, (uint64_t)(g.N / 2), (uint64_t)c_rows,
-                         (uint64_t)g.ldc, 16, 32, CU_TENSOR_MAP_SWIZZLE_NONE)
-              : make_map(&tc, OUT == OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                         g.c, (uint64_t)g.N, (uint64_t)c_rows, (uint64_t)g.ldc * (OUT == OUT_BF16 ? 2 : 4),
-                         OUT == OUT_BF16 ? 64 : 32, 32, CU_TENSOR_MAP_SWIZZLE_128B)) ||
-        // scale atoms as a 3D tensor [128-row tile][K atom][512 bytes = 128 x 32-bit]:
-        // one box holds NATOM consecutive atoms of one (A) or NRT (B) row tiles
-        !make_map_3d(&tsa, g.a_scales, (uint64_t)katoms, (uint64_t)a_tiles, Cfg::NATOM, 1) ||
-        !make_map_3d(&tsb, g.b_scales, (uint64_t)katoms, (uint64_t)(G * b_tiles), Cfg::NATOM, Cfg::NRT))
+    CUtensorMap ta, tb, tc, tz, tsa, tsb;
+    constexpr CUtensorMapDataType BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    constexpr CUtensorMapSwizzle SW128 = CU_TENSOR_MAP_SWIZZLE_128B;
+    const uint64_t kbytes = (uint64_t)(g.K / Cfg::KPB), N = (uint64_t)g.N, ldc = (uint64_t)g.ldc;
+    bool ok = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a_codes, kbytes, (uint64_t)g.M, (uint64_t)g.lda, CHUNK, BM,
+                       SW128) &&
+              make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b_codes, kbytes, (uint64_t)G * N, (uint64_t)g.ldb, CHUNK,
+                       BN / 2, SW128);
+    if constexpr (OUT == OUT_MX)
+        ok = ok && make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.c, N / 2, (uint64_t)c_rows, ldc, 16, 32,
+                            CU_TENSOR_MAP_SWIZZLE_NONE);
+    else if constexpr (OUT == OUT_GATED)
+        ok = ok && make_map(&tc, BF, g.c, N / 2, (uint64_t)c_rows, ldc * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    else if constexpr (OUT == OUT_GATED_BWD)
+        ok = ok && make_map(&tc, BF, g.c, 2 * N, (uint64_t)c_rows, ldc * 2, 64, 32, SW128);
+    else if constexpr (OUT == OUT_BF16)
+        ok = ok && make_map(&tc, BF, g.c, N, (uint64_t)c_rows, ldc * 2, 64, 32, SW128);
+    else
+        ok = ok && make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.c, N, (uint64_t)c_rows, ldc * 4, 32, 32, SW128);
+    if (!ok) return MXFP4_ERR_CUDA;
+    tz = tsa = tsb = tc;                       // never used where an operand below does not exist
+    if ((OUT == OUT_GATED || OUT == OUT_GATED_BWD) && g.z &&
+        !make_map(&tz, BF, g.z, OUT == OUT_GATED ? N : 2 * N, (uint64_t)c_rows, (uint64_t)g.ldz * 2, 64, 32, SW128))
         return MXFP4_ERR_CUDA;
+    // scale atoms as a 3D tensor [128-row tile][K atom][512 bytes = 128 x 32-bit]:
+    // one box holds NATOM consecutive atoms of one (A) or NRT (B) row tiles
+    if constexpr (!Cfg::I8)
+        if (!make_map_3d(&tsa, g.a_scales, (uint64_t)katoms, (uint64_t)a_tiles, Cfg::NATOM, 1) ||
+            !make_map_3d(&tsb, g.b_scales, (uint64_t)katoms, (uint64_t)(G * b_tiles), Cfg::NATOM, Cfg::NRT))
+            return MXFP4_ERR_CUDA;
     if (set_smem_attr<Cfg, MODE, OUT>() != cudaSuccess) return MXFP4_ERR_CUDA;
     GemmParams p{};
     p.M = g.M; p.N = g.N; p.K = g.K;
@@ -829,6 +1146,9 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     p.c_katoms = (g.N / 32 + 3) / 4;
     p.group_offsets = g.offsets; p.group_sizes = g.sizes; p.num_groups = g.G;
     p.a_amax = g.a_amax; p.b_amax = g.b_amax;
+    p.a_tok = g.a_tok; p.b_chan = g.b_chan;
+    p.z = g.z; p.ldz = g.ldz;
+    p.act_alpha = g.alpha; p.act_limit = g.limit; p.act_beta = g.beta;
     p.wait_limit_ns = g_wait_limit_ns;
     const int pairs_max = sm_count() / 2;
     int pairs = pairs_max;
@@ -837,7 +1157,7 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
         pairs = (int)(tiles < pairs_max ? tiles : pairs_max);
     }
     const cudaError_t e = launch_pdl(mxfp4_gemm_kernel<Cfg, MODE, OUT>, dim3((unsigned)(2 * pairs)), dim3(NUM_THREADS),
-                                     (size_t)Cfg::SMEM_BYTES, s, ta, tb, tc, tsa, tsb, p);
+                                     (size_t)Cfg::SMEM_BYTES, s, ta, tb, tc, tsa, tsb, tz, p);
     return e == cudaSuccess ? 0 : MXFP4_ERR_CUDA;
 }
 
@@ -898,6 +1218,34 @@ int launch_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scal
                       int64_t N, int64_t K, float *c, int64_t ldc, cudaStream_t s) {
     GemmArgs g{a_codes, a_scales, b_codes, b_scales, lda, ldb, M, N, K, ldc, c, nullptr, nullptr, 1, a_amax, b_amax};
     return launch_cfg<NvCfg, MODE_DENSE>(g, s);
+}
+
+// Gated products: the activation of column pairs of A B^T (forward), or dz from
+// dh = A B^T and z (backward); offsets null for the dense forms.
+int launch_gated(const GatedArgs &a, cudaStream_t s) {
+    GemmArgs g{a.a_codes, a.a_scales, a.b_codes, a.b_scales, a.lda, a.ldb, a.M, a.N, a.K, a.ld_out, a.out, a.offsets,
+               a.sizes, a.offsets ? a.G : 1};
+    g.z = a.z;
+    g.ldz = a.ldz;
+    g.alpha = a.alpha;
+    g.limit = a.limit;
+    g.beta = a.beta;
+    if (a.backward)
+        return a.offsets ? launch_cfg<BwdCfg, MODE_GROUPED_M, OUT_GATED_BWD>(g, s)
+                         : launch_cfg<BwdCfg, MODE_DENSE, OUT_GATED_BWD>(g, s);
+    return a.offsets ? launch_cfg<DefaultCfg, MODE_GROUPED_M, OUT_GATED>(g, s)
+                     : launch_cfg<DefaultCfg, MODE_DENSE, OUT_GATED>(g, s);
+}
+
+int launch_int8_gemm(const Int8Args &a, cudaStream_t s) {
+    GemmArgs g{reinterpret_cast<const uint8_t *>(a.a), nullptr, reinterpret_cast<const uint8_t *>(a.b), nullptr, a.lda,
+               a.ldb, a.M, a.N, a.K, a.ldc, a.c, a.offsets, a.sizes, a.offsets ? a.G : 1};
+    g.a_tok = a.a_scales;
+    g.b_chan = a.b_scales;
+    if (a.offsets)
+        return a.bf16 ? launch_cfg<I8GroupedCfg, MODE_GROUPED_M, OUT_BF16>(g, s)
+                      : launch_cfg<I8GroupedCfg, MODE_GROUPED_M, OUT_F32>(g, s);
+    return a.bf16 ? launch_cfg<I8Cfg, MODE_DENSE, OUT_BF16>(g, s) : launch_cfg<I8Cfg, MODE_DENSE, OUT_F32>(g, s);
 }
 
 int get_error(cudaStream_t s) {
