@@ -447,6 +447,8 @@ MXFP4_API int mxfp4_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_
  * rounded once (nearest even).  z (optional, NULL = not kept): bf16 [.., N]
  * (ldz), the accumulators rounded once, for the backward pass.  Rows outside
  * the groups are left as they were.
+ * A dense call of few rows (M <= 4) may run a kernel of its own that streams B
+ * once; its sums differ from the tile kernel's in their last bits.
  *
  * Requirements: as mxfp4_gemm / mxfp4_grouped_gemm; N even; h and z 16-byte
  * aligned, ldh % 8 == 0, ldz % 8 == 0, not overlapping; alpha and beta finite,
@@ -493,7 +495,7 @@ MXFP4_API int mxfp4_grouped_gated_gemm_backward(const uint8_t *a_codes, int64_t 
  * mxfp4_int8_quantize -- bf16 x[rows, cols] to signed 8-bit codes with one FP32
  * scale per row (a token of activations, an output channel of a weight):
  *     a = max(amax of the row, 2^-100), scales[row] = fp32(a / 127),
- *     codes = nearest-even of fp32(x * fp32(127 / a)), within +-127.
+ *     codes = nearest-even of fp32(x * fp32(127 * fp32(1 / a))), within +-127.
  * The value of a code is code * scale.  A NaN or Inf in a row gives it the
  * scale NaN and codes 0.  codes [rows, cols] (ld_codes bytes), scales [rows].
  * Requirements: rows, cols > 0; cols % 16 == 0; x and codes 16-byte aligned,

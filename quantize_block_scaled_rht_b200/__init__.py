@@ -549,106 +549,137 @@ def mxfp4_scales_to_mma(scales: torch.Tensor, rows: int, k: int, two_d: bool = F
 # the stream they run on.
 # ---------------------------------------------------------------------------
 
-def _call(fn, what: str, dev: torch.device, stream, *args) -> None:
-    """fn(*args, stream) with `dev` current; stream None = its current stream."""
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, _stream(stream))
+# Host time counts where one token's kernels take a few microseconds, so the
+# common path (tensors on the current device, its current stream) does nothing
+# twice.
+
+def _run(fn, what: str, idx: int, stream, *args) -> None:
+    """fn(*args, stream) on device idx; stream None = its current stream."""
+    if torch._C._cuda_getDevice() == idx:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream))
-    if rc != MXFP4_OK:
+        with torch.cuda.device(idx):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else _stream(stream))
+    if rc:
         raise MXFP4Error(rc, what)
 
 
-def _device(what: str, stream, *ts: Optional[torch.Tensor]) -> torch.device:
-    """The one CUDA device of the tensors (None skipped), checked against the stream's."""
-    dev = ts[0].device
-    if dev.type != "cuda":
-        raise ValueError("libmxfp4 takes CUDA tensors (device pointers)")
+def _device(what: str, stream, *ts: torch.Tensor) -> int:
+    """Index of the one CUDA device of the tensors, checked against the stream's."""
+    idx = ts[0].get_device()
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{what}: tensors on different devices: {dev} and {t.device}")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"{what}: stream of {stream.device} for tensors on {dev}")
-    return dev
+        if t.get_device() != idx:
+            raise ValueError(f"{what}: tensors on different devices: {ts[0].device} and {t.device}")
+    if idx < 0:
+        raise ValueError("libmxfp4 takes CUDA tensors (device pointers)")
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device.index != idx:
+        raise ValueError(f"{what}: stream of {stream.device} for tensors on {ts[0].device}")
+    return idx
 
 
-def _empty(shape, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, idx: int, stream) -> torch.Tensor:
     """An output tensor that belongs to the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=idx)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        stream = torch.cuda.ExternalStream(int(stream), device=idx)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=idx)
 
 
-def _empty_rows(rows: int, cols: int, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
-    """_empty whose rows start on 16-byte boundaries, as the kernels store them
-    (a view of a wider tensor where cols alone does not give that)."""
-    per = 16 // dtype.itemsize
-    if cols % per == 0:
-        return _empty((rows, cols), dtype, dev, stream)
-    return _empty((rows, (cols + per - 1) // per * per), dtype, dev, stream)[:, :cols]
+def _empty_rows(rows: int, cols: int, dtype: torch.dtype, idx: int, stream):
+    """(_empty, its row stride) with rows that start on 16-byte boundaries, as the
+    kernels store them: a view of a wider tensor where cols alone does not give that."""
+    per = 8 if dtype is torch.bfloat16 else 4
+    if not cols % per:
+        return _empty((rows, cols), dtype, idx, stream), cols
+    ld = (cols + per - 1) // per * per
+    return _empty((rows, ld), dtype, idx, stream)[:, :cols], ld
 
 
-def _check_rows(t: torch.Tensor, what: str, dtype, shape) -> None:
-    """A 2-D row-major tensor (any row stride) of this type and shape."""
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape != shape or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a row-major tensor of shape {tuple(shape)}, got {tuple(t.shape)} with strides "
-                         f"{t.stride()}")
+def _rows(t: torch.Tensor, what: str, dtypes: tuple, shape=None) -> int:
+    """Checks a 2-D row-major tensor of one of these types (and this shape);
+    returns its row stride.  A single row's stride is never used, and torch may
+    leave any: it stands at a 16-byte multiple that covers the row."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    got = t.shape
+    if len(got) != 2 or (shape is not None and got != shape):
+        raise ValueError(f"{what} must be a row-major tensor of shape {tuple(shape or ('rows', 'columns'))}, got {tuple(got)}")
+    ld, step = t.stride()
+    if step != 1 and got[1] > 1:
+        raise ValueError(f"{what} must be row-major, got strides {t.stride()}")
+    return ld if got[0] > 1 else (got[1] + 15) // 16 * 16
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride; a single row's is never used and torch may leave any, so it
-    stands at a 16-byte multiple that covers the row."""
-    return (t.shape[1] + 15) // 16 * 16 if t.shape[0] == 1 else t.stride(0)
-
-
-def _check_groups(what: str, offsets: torch.Tensor, sizes: torch.Tensor, b: torch.Tensor) -> int:
+def _groups(what: str, offsets: torch.Tensor, sizes: torch.Tensor, b: torch.Tensor) -> int:
     if offsets.dtype != torch.int32 or sizes.dtype != torch.int32 or offsets.dim() != 1 or sizes.dim() != 1 or \
             not offsets.is_contiguous() or not sizes.is_contiguous():
         raise ValueError(f"{what}: group_offsets and group_sizes must be contiguous 1-D int32 tensors")
     G = sizes.numel()
     if offsets.numel() != G + 1:
         raise ValueError(f"{what}: {G} group sizes need {G + 1} group offsets, got {offsets.numel()}")
-    if b.dim() != 3 or b.shape[0] != G or b.stride(2) != 1 or (G > 1 and b.stride(0) != b.shape[1] * b.stride(1)):
+    if b.shape[0] != G or (G > 1 and b.stride(0) != b.shape[1] * b.stride(1)):
         raise ValueError(f"{what}: B must be [{G}, N, K] with contiguous groups, got {tuple(b.shape)} with strides "
                          f"{b.stride()}")
     return G
+
+
+def _b_rows(b: torch.Tensor, what: str, dtype: torch.dtype, grouped: bool) -> int:
+    """Checks B, [N, K] or [G, N, K] codes with contiguous rows; returns its row stride."""
+    if b.dtype != dtype:
+        raise ValueError(f"{what}: codes must be {dtype} tensors")
+    if b.dim() != (3 if grouped else 2) or b.stride(-1) != 1:
+        raise ValueError(f"{what}: B must be row-major codes {'[G, N, K]' if grouped else '[N, K]'}, got {tuple(b.shape)} "
+                         f"with strides {b.stride()}")
+    ld = b.stride(-2)
+    return ld if grouped or b.shape[0] > 1 else (b.shape[1] + 15) // 16 * 16
+
+
+def _scales_ready(t: torch.Tensor, name: str, what: str, rows: int, K: int, groups: int = 1) -> int:
+    """Checks the GEMM-ready scales of `groups` operands of rows x K; returns the pointer."""
+    need = groups * ((rows + 127) // 128) * ((K // 32 + 3) // 4) * 512
+    if t.dtype != torch.uint8 or t.dim() != 1 or t.numel() < need or not t.is_contiguous():
+        raise ValueError(f"{name}: {what} must be the GEMM-ready (SCALES_MMA) layout, a contiguous 1-D uint8 tensor of at "
+                         f"least {need} bytes; got {t.dtype} {tuple(t.shape)} (quantize with scale_layout=SCALES_MMA or "
+                         f"convert with mxfp4_scales_to_mma)")
+    return t.data_ptr()
+
+
+_U8, _I8, _BF16, _BF16_F32 = (torch.uint8,), (torch.int8,), (torch.bfloat16,), (torch.bfloat16, torch.float32)
 
 
 def _gated(name: str, a_codes, a_scales, groups, b_codes, b_scales, K, alpha, limit, beta, z, keep_z, out, stream):
     """The four gated entry points: z None or a tensor to write (forward), or the
     kept pre-activations (backward: keep_z is None)."""
     grouped, backward = groups is not None, keep_z is None
-    if a_codes.dim() != 2 or a_codes.stride(1) != 1 or b_codes.dim() != (3 if grouped else 2) or b_codes.stride(-1) != 1:
-        raise ValueError(f"{name}: codes must be row-major, A [M, K/2] and B {'[G, N, K/2]' if grouped else '[N, K/2]'}")
-    M, N = a_codes.shape[0], b_codes.shape[-2]
-    G = _check_groups(name, *groups, b_codes) if grouped else 1
-    _check_operand(a_codes, a_scales, M, K, "A")
-    _check_operand(b_codes, b_scales, N, K, "B", groups=G)
-    if not a_scales.is_contiguous() or not b_scales.is_contiguous():
-        raise ValueError(f"{name}: scales must be contiguous")
+    lda = _rows(a_codes, "A", _U8)
+    ldb = _b_rows(b_codes, name, torch.uint8, grouped)
+    (M, ka), (N, kb) = a_codes.shape, b_codes.shape[-2:]
+    if 2 * ka < K or 2 * kb < K:
+        raise ValueError(f"{name}: codes hold {2 * min(ka, kb)} elements per row, K = {K}")
+    G = _groups(name, *groups, b_codes) if grouped else 1
+    first = (a_codes.data_ptr(), lda, _scales_ready(a_scales, name, "a_scales", M, K))
+    second = (b_codes.data_ptr(), ldb, _scales_ready(b_scales, name, "b_scales", N, K, G))
     if not backward and N % 2:
         raise ValueError(f"{name}: B holds gate and up rows in turn, N = {N} is odd")
-    oshape, zshape = (M, 2 * N if backward else N // 2), (M, 2 * N if backward else N)
+    ocols, zcols = (2 * N, 2 * N) if backward else (N // 2, N)
+    used = [a_codes, a_scales, b_codes, b_scales, *(groups or ())]
     if z is not None:
-        _check_rows(z, "z", torch.bfloat16, zshape)
+        ldz = _rows(z, "z", _BF16, (M, zcols))
+        used.append(z)
     if out is not None:
-        _check_rows(out, "out", torch.bfloat16, oshape)
-    dev = _device(name, stream, a_codes, a_scales, b_codes, b_scales, z, out, *(groups or ()))
+        ldo = _rows(out, "out", _BF16, (M, ocols))
+        used.append(out)
+    idx = _device(name, stream, *used)
     if out is None:
-        out = _empty_rows(*oshape, torch.bfloat16, dev, stream)
+        out, ldo = _empty_rows(M, ocols, torch.bfloat16, idx, stream)
     if keep_z and z is None:
-        z = _empty_rows(*zshape, torch.bfloat16, dev, stream)
-    first = (a_codes.data_ptr(), _ld(a_codes), a_scales.data_ptr())
-    second = (b_codes.data_ptr(), b_codes.stride(-2), b_scales.data_ptr())
+        z, ldz = _empty_rows(M, zcols, torch.bfloat16, idx, stream)
     rows = (M, groups[0].data_ptr(), groups[1].data_ptr(), G, *second, N, K) if grouped else (*second, M, N, K)
-    pz, po = (None if z is None else z.data_ptr(), 0 if z is None else _ld(z)), (out.data_ptr(), _ld(out))
-    _call(getattr(lib(), name), name, dev, stream, *first, *rows, alpha, limit, beta, *(pz + po if backward else po + pz))
+    pz, po = (None, 0) if z is None else (z.data_ptr(), ldz), (out.data_ptr(), ldo)
+    _run(getattr(_lib or lib(), name), name, idx, stream, *first, *rows, alpha, limit, beta,
+         *(pz + po if backward else po + pz))
     return out, z
 
 
@@ -708,50 +739,49 @@ def mxfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Quantized] = None, st
     """Signed 8-bit codes and one scale per row of a 2-D bf16 tensor: activations
     by token, a weight [N, K] by output channel (see mxfp4_int8_quantize in
     include/mxfp4.h)."""
-    if x.dim() != 2:
-        raise ValueError("x must be a 2-D bfloat16 tensor")
-    _check_rows(x, "x", torch.bfloat16, x.shape)
+    ld = _rows(x, "x", _BF16)
     rows, cols = x.shape
-    if out is not None:
-        _check_rows(out.codes, "out.codes", torch.int8, x.shape)
-        if out.scales.dtype != torch.float32 or out.scales.shape != (rows,) or not out.scales.is_contiguous():
-            raise ValueError(f"out.scales must be a contiguous float32 tensor of shape ({rows},)")
-    dev = _device("mxfp4_int8_quantize", stream, x, *((out.codes, out.scales) if out is not None else ()))
     if out is None:
-        out = Int8Quantized(_empty((rows, cols), torch.int8, dev, stream), _empty((rows,), torch.float32, dev, stream))
-    _call(lib().mxfp4_int8_quantize, "mxfp4_int8_quantize", dev, stream, x.data_ptr(), rows, cols, _ld(x),
-          out.codes.data_ptr(), _ld(out.codes), out.scales.data_ptr())
+        idx = _device("mxfp4_int8_quantize", stream, x)
+        codes, scales = _empty((rows, cols), torch.int8, idx, stream), _empty((rows,), torch.float32, idx, stream)
+        ldc, out = cols, Int8Quantized(codes, scales)
+    else:
+        codes, scales = out.codes, out.scales
+        ldc = _rows(codes, "out.codes", _I8, (rows, cols))
+        _token_scales(scales, "out.scales", (rows,))
+        idx = _device("mxfp4_int8_quantize", stream, x, codes, scales)
+    _run((_lib or lib()).mxfp4_int8_quantize, "mxfp4_int8_quantize", idx, stream, x.data_ptr(), rows, cols, ld,
+         codes.data_ptr(), ldc, scales.data_ptr())
     return out
+
+
+def _token_scales(t: torch.Tensor, what: str, shape: tuple) -> int:
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _int8_gemm(name: str, a_codes, a_scales, groups, b_codes, b_scales, out_dtype, out, stream) -> torch.Tensor:
     grouped = groups is not None
-    if a_codes.dtype != torch.int8 or b_codes.dtype != torch.int8:
-        raise ValueError(f"{name}: codes must be int8 tensors")
-    if a_codes.dim() != 2 or a_codes.stride(1) != 1 or b_codes.dim() != (3 if grouped else 2) or b_codes.stride(-1) != 1:
-        raise ValueError(f"{name}: codes must be row-major, A [M, K] and B {'[G, N, K]' if grouped else '[N, K]'}")
-    M, K = a_codes.shape
-    N = b_codes.shape[-2]
-    if b_codes.shape[-1] != K:
-        raise ValueError(f"{name}: A has K = {K}, B {b_codes.shape[-1]}")
-    G = _check_groups(name, *groups, b_codes) if grouped else 1
-    for t, shape, what in ((a_scales, (M,), "a_scales"), (b_scales, (G, N) if grouped else (N,), "b_scales")):
-        if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: {what} must be a contiguous float32 tensor of shape {shape}, got {t.dtype} "
-                             f"{tuple(t.shape)}")
-    if out is not None:
-        _check_rows(out, "out", (torch.bfloat16, torch.float32), (M, N))
-        out_dtype = out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name}: out_dtype must be bfloat16 or float32")
-    dev = _device(name, stream, a_codes, a_scales, b_codes, b_scales, out, *(groups or ()))
+    lda = _rows(a_codes, "A", _I8)
+    ldb = _b_rows(b_codes, name, torch.int8, grouped)
+    (M, K), (N, kb) = a_codes.shape, b_codes.shape[-2:]
+    if kb != K:
+        raise ValueError(f"{name}: A has K = {K}, B {kb}")
+    G = _groups(name, *groups, b_codes) if grouped else 1
+    first = (a_codes.data_ptr(), lda, _token_scales(a_scales, "a_scales", (M,)))
+    second = (b_codes.data_ptr(), ldb, _token_scales(b_scales, "b_scales", (G, N) if grouped else (N,)))
     if out is None:
-        out = _empty_rows(M, N, out_dtype, dev, stream)
-    first = (a_codes.data_ptr(), _ld(a_codes), a_scales.data_ptr())
-    second = (b_codes.data_ptr(), (K + 15) // 16 * 16 if N == 1 and not grouped else b_codes.stride(-2), b_scales.data_ptr())
+        if out_dtype not in _BF16_F32:
+            raise ValueError(f"{name}: out_dtype must be bfloat16 or float32")
+        idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales, *(groups or ()))
+        out, ldo = _empty_rows(M, N, out_dtype, idx, stream)
+    else:
+        ldo = _rows(out, "out", _BF16_F32, (M, N))
+        idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales, out, *(groups or ()))
     rows = (M, groups[0].data_ptr(), groups[1].data_ptr(), G, *second, N, K) if grouped else (*second, M, N, K)
-    _call(getattr(lib(), name), name, dev, stream, *first, *rows, out.data_ptr(), _ld(out),
-          OUT_F32 if out_dtype == torch.float32 else OUT_BF16)
+    _run(getattr(_lib or lib(), name), name, idx, stream, *first, *rows, out.data_ptr(), ldo,
+         OUT_F32 if out.dtype == torch.float32 else OUT_BF16)
     return out
 
 
@@ -780,21 +810,22 @@ def mxfp4_dropout(x: torch.Tensor, p: float, seed: int, elem_offset: int = 0, re
     from the Philox stream of (seed, element index) and never stored (see
     mxfp4_dropout in include/mxfp4.h).  The gradient is the same call on dY.
     out may be x or residual itself."""
-    if x.dim() != 2:
-        raise ValueError("x must be a 2-D bfloat16 or float32 tensor")
-    _check_rows(x, "x", (torch.bfloat16, torch.float32), x.shape)
-    for t, what in ((residual, "residual"), (out, "out")):
-        if t is not None:
-            _check_rows(t, what, x.dtype, x.shape)
+    ld = _rows(x, "x", _BF16_F32)
+    kind, shape, res = (x.dtype,), x.shape, (None, 0)
+    used = [x]
+    if residual is not None:
+        res = (residual.data_ptr(), _rows(residual, "residual", kind, shape))
+        used.append(residual)
+    if out is not None:
+        ldo = _rows(out, "out", kind, shape)
+        used.append(out)
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be within [0, 1], got {p}")
-    dev = _device("mxfp4_dropout", stream, x, residual, out)
+    idx = _device("mxfp4_dropout", stream, *used)
     if out is None:
-        out = _empty(x.shape, x.dtype, dev, stream)
-    res = (None, 0) if residual is None else (residual.data_ptr(), _ld(residual))
-    _call(lib().mxfp4_dropout, "mxfp4_dropout", dev, stream, x.data_ptr(), _ld(x), *res, x.shape[0], x.shape[1],
-          OUT_F32 if x.dtype == torch.float32 else OUT_BF16, p, seed & 0xFFFFFFFFFFFFFFFF, elem_offset, out.data_ptr(),
-          _ld(out))
+        out, ldo = _empty(shape, x.dtype, idx, stream), shape[1]
+    _run((_lib or lib()).mxfp4_dropout, "mxfp4_dropout", idx, stream, x.data_ptr(), ld, *res, shape[0], shape[1],
+         OUT_F32 if x.dtype == torch.float32 else OUT_BF16, p, seed & 0xFFFFFFFFFFFFFFFF, elem_offset, out.data_ptr(), ldo)
     return out
 
 

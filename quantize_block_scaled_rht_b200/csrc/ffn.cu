@@ -24,8 +24,9 @@ __device__ __forceinline__ void st_v2(void *p, uint32_t a, uint32_t b) {
 
 // ---------------------------------------------------------------------------
 // int8 token quantizer: per row a = max(amax, 2^-100), scale = a / 127, codes
-// RNE(x * (127 / a)).  The floor keeps 127 / a finite; a NaN or Inf anywhere in
-// the row gives the scale NaN and codes 0.
+// RNE(x * i) with i = 127 * (1 / a), each step rounded to FP32 (i is within 1.5
+// steps of 2^-24 of 127 / a, so |x i| stays below 127.5).  The floor keeps 1 / a
+// finite; a NaN or Inf anywhere in the row gives the scale NaN and codes 0.
 //
 // Bound by HBM (2 B read, 1 B written per element).  T threads hold one row in
 // registers (V 16-byte vectors each), so it is read once; a row that does not
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 / T * T : T)
     int8_t *dst = codes + row * ld_codes;
     const bool finite = a < 0x7F800000u;
     const float amax = fmaxf(__uint_as_float(a), __uint_as_float(0x0D800000u));   // 2^-100
-    const float inv = finite ? __fdiv_rn(127.0f, amax) : 0.0f;
+    const float inv = finite ? __fmul_rn(__fdiv_rn(1.0f, amax), 127.0f) : 0.0f;
     if (tid == 0) scales[row] = finite ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7FC00000u);
     if constexpr (V > 0) {
 #pragma unroll

@@ -20,36 +20,65 @@ namespace mxfp4 {
 struct GatedAct {
     float alpha, limit, beta;
 
-    // 1 / (1 + 2^(-alpha log2(e) g)) with the hardware's base-2 exponential and
-    // reciprocal: the product's rounding moves the exponent by at most
-    // |alpha g| 2^-23, which for the |g| where s is not yet 0 or 1 leaves a
-    // relative error under 1e-5, a hundredth of bf16's half-step.
-    __device__ __forceinline__ float sigmoid(float g) const {
-        float e, s;
-        const float x = __fmul_rn(g, __fmul_rn(alpha, -1.44269504f));
-        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x));
-        const float d = __fadd_rn(1.0f, e);
-        asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(d));
-        return s;
+    // s = 1 / (1 + 2^(-alpha log2(e) g)) of N values with the hardware's base-2
+    // exponential and reciprocal: the product's rounding moves the exponent by
+    // at most |alpha g| 2^-23, which for the |g| where s is not yet 0 or 1 leaves
+    // a relative error under 1e-5, a hundredth of bf16's half-step.  Both flush
+    // subnormals (an exponential below 2^-126 leaves s = 1, a sum above 2^126
+    // s = 0); the forms that keep them cost a branch each.  One step for all N
+    // values at a time: a warp of the GEMM's epilogue has a scheduler to itself,
+    // so only independent values hide the latency of a step.
+    template <int N>
+    __device__ __forceinline__ void sigmoid(const float *g, float *s) const {
+        const float k = __fmul_rn(alpha, -1.44269504f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = __fmul_rn(g[i], k);
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = __fadd_rn(s[i], 1.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
     }
-    // Comparisons, not fmin / fmax, so that a NaN goes through.
-    __device__ __forceinline__ float clamp_gate(float z) const { return z > limit ? limit : z; }
+    // One instruction per bound; a NaN goes through.
+    __device__ __forceinline__ float clamp_gate(float z) const {
+        float r;
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(limit));
+        return r;
+    }
     __device__ __forceinline__ float clamp_up(float z) const {
-        return z > limit ? limit : (z < -limit ? -limit : z);
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(clamp_gate(z)), "f"(-limit));
+        return r;
     }
-    __device__ __forceinline__ float forward(float zg, float zu) const {
-        const float g = clamp_gate(zg);
-        return __fmul_rn(__fmul_rn(g, sigmoid(g)), __fadd_rn(clamp_up(zu), beta));
+    // N pairs (zg, zu) in v, FP32 bits, to N values h.
+    template <int N>
+    __device__ __forceinline__ void forward(const uint32_t *v, float *h) const {
+        float s[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[i] = clamp_gate(__uint_as_float(v[2 * i]));
+        sigmoid<N>(h, s);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            h[i] = __fmul_rn(__fmul_rn(h[i], s[i]), __fadd_rn(clamp_up(__uint_as_float(v[2 * i + 1])), beta));
     }
-    // dh and the packed bf16 pair (zg low, zu high) to the packed pair (dzg, dzu).
-    __device__ __forceinline__ uint32_t backward(float dh, uint32_t z) const {
-        const float zg = bf16lo(z), zu = bf16hi(z);
-        const float g = clamp_gate(zg), u = clamp_up(zu), s = sigmoid(g);
-        const float t = __fmaf_rn(__fmul_rn(alpha, g), __fsub_rn(1.0f, s), 1.0f);
-        const float hs = __fmul_rn(dh, s);
-        const float dg = __fmul_rn(__fmul_rn(hs, __fadd_rn(u, beta)), t);
-        const float du = __fmul_rn(hs, g);
-        return pack_bf16x2(zg > limit ? 0.0f : dg, fabsf(zu) > limit ? 0.0f : du);
+    // N values dh (FP32 bits) and packed bf16 pairs z (zg low, zu high), the
+    // pairs replaced by (dzg, dzu).
+    template <int N>
+    __device__ __forceinline__ void backward(const uint32_t *dh, uint32_t *z) const {
+        float g[N], s[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = clamp_gate(bf16lo(z[i]));
+        sigmoid<N>(g, s);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float zu = bf16hi(z[i]);
+            const float t = __fmaf_rn(__fmul_rn(alpha, g[i]), __fsub_rn(1.0f, s[i]), 1.0f);
+            const float hs = __fmul_rn(__uint_as_float(dh[i]), s[i]);
+            const float dg = __fmul_rn(__fmul_rn(hs, __fadd_rn(clamp_up(zu), beta)), t);
+            const float du = __fmul_rn(hs, g[i]);
+            z[i] = pack_bf16x2(bf16lo(z[i]) > limit ? 0.0f : dg, fabsf(zu) > limit ? 0.0f : du);
+        }
     }
 };
 
@@ -76,6 +105,17 @@ struct Int8Args {
     const int32_t *offsets, *sizes;
     int G;
 };
+
+// Products of few rows (rows.cu): at most ROWS_MAX, handled 1, 2 or 4 at a
+// time; the gated one also needs that many rows of A, one byte per element and
+// scale, in 48 KB of shared memory (less what the kernel has besides).
+constexpr int64_t ROWS_MAX = 4;
+inline int64_t rows_handled(int64_t M) { return M <= 2 ? M : 4; }
+inline bool gated_rows_fit(int64_t M, int64_t K) {
+    return M <= ROWS_MAX && rows_handled(M) * (K + K / 32) <= 47 * 1024;
+}
+int launch_gated_rows(const GatedArgs &a, cudaStream_t s);
+int launch_int8_rows(const Int8Args &a, cudaStream_t s);
 
 int launch_gated(const GatedArgs &a, cudaStream_t s);
 int launch_int8_gemm(const Int8Args &a, cudaStream_t s);

@@ -43,10 +43,8 @@ namespace mxfp4 {
 
 constexpr int BM = 128;                               // rows per CTA
 constexpr int CHUNK = 128;                            // K bytes per swizzled chunk (256 E2M1 = 8 scale blocks)
-constexpr int EPI_WARPS = 4;
 constexpr int EPI_BUF = 32 * 32 * 4;                  // 32 rows x 32 FP32
 constexpr int BAR_BYTES = 256;
-constexpr int NUM_THREADS = 192;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_GROUPS = 1024;
 constexpr int MAX_STAGES = 8;
@@ -58,15 +56,21 @@ constexpr int MAX_STAGES = 8;
 // of a 128-row tile: 128 K-elements for MXFP4, 64 for NVFP4.  KIND_I8: signed
 // 8-bit integers (kind::i8, exact 32-bit integer sums), one element per byte and
 // no scale atoms; the token and channel scales go in with the epilogue.
-// EPI_BUFS: 4 KB staging buffers per epilogue warp.
+// EPI_BUFS: 4 KB staging buffers per epilogue warp.  EPI_WARPS: 4, or 8 for the
+// epilogues with real arithmetic: a warp may read only the quarter of the tensor
+// memory lanes that its index selects, so two warps share a quarter and take
+// its column steps in turn.
 constexpr int KIND_MX = 0, KIND_NV = 1, KIND_I8 = 2;
-template <int BN_, int STAGES_, int KCH_, int KIND_ = KIND_MX, int EPI_BUFS_ = 2>
+template <int BN_, int STAGES_, int KCH_, int KIND_ = KIND_MX, int EPI_BUFS_ = 2, int EPI_WARPS_ = 4>
 struct TileCfg {
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
     static constexpr int KCH = KCH_;
     static constexpr bool NV = KIND_ == KIND_NV, I8 = KIND_ == KIND_I8;
     static constexpr int EPI_BUFS = EPI_BUFS_;
+    static constexpr int EPI_WARPS = EPI_WARPS_;
+    static constexpr int SPLIT = EPI_WARPS / 4;       // warps per lane quarter
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * EPI_BUF;
     static constexpr int KPB = I8 ? 1 : 2;            // K-elements per byte
     static constexpr int KMMA = 32 * KPB;             // K-elements per instruction (32 bytes)
@@ -96,8 +100,9 @@ struct TileCfg {
     // kind::i8: signed A and B (1), 32-bit integer accumulators (2 at bit 4).
     static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
                                       (I8 ? 2u << 4 : (NV ? 0u : 1u) << 23) | ((uint32_t)(256 >> 4) << 24);
-    static_assert(BN == 128 || BN == 192 || (I8 && (BN == 64 || BN == 256)), "tile width");
+    static_assert(BN == 128 || BN == 192 || (I8 && BN == 256), "tile width");
     static_assert(KCH == 1 || KCH == 2, "chunks per stage");
+    static_assert(EPI_WARPS == 4 || EPI_WARPS == 8, "epilogue warps");
     static_assert(STAGES <= MAX_STAGES, "stages");
     static_assert(SF_COL + 2 * SF_STAGE_COLS <= ACC1_COL, "TMEM layout");
     static_assert(A_CHUNK % 1024 == 0 && B_CHUNK % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle alignment");
@@ -113,17 +118,20 @@ constexpr int OUT_F32 = 0, OUT_BF16 = 1, OUT_MX = 2, OUT_GATED = 3, OUT_GATED_BW
 
 using DefaultCfg = TileCfg<192, 3, 2>;
 using NvCfg = TileCfg<192, 5, 1, KIND_NV>;
-// The backward pass streams z in and dz out through the same staging buffers:
-// four per warp keep two loads ahead of the box being computed, paid for with a
-// ring of 5 x 256 instead of 3 x 512 K-elements.
-using BwdCfg = TileCfg<192, 5, 1, KIND_MX, 4>;
-// int8: twice the operand bytes per K of MXFP4 at half the MMA rate, so L2
-// traffic per MMA cycle is the same; without scale factors in tensor memory two
-// 256-column accumulators fit, and a 256 x 256 tile reads 1/8 fewer operand
-// bytes per product than 256 x 192.
-using I8Cfg = TileCfg<256, 3, 2, KIND_I8>;
+// The gated epilogues take eight warps.  Forward: one staging buffer each, which
+// keeps the 3 x 512 ring (4096 x 5760 x 2880, h alone: 35.1 us, the bf16
+// product's time; 4 warps and two buffers 48.8, 8 warps and two buffers on a
+// ring of 5 x 256 40.2).  Backward: three buffers carry z in and dz out, paid for
+// with a ring of 4 x 256 (4096 x 2880 x 2880: 38.3 us; 4 warps, four buffers and
+// a ring of 5 x 256 43.3).
+using GatedCfg = TileCfg<192, 3, 2, KIND_MX, 1, 8>;
+using BwdCfg = TileCfg<192, 4, 1, KIND_MX, 3, 8>;
+// int8: without scale factors in tensor memory two 256-column accumulators fit,
+// and a 256 x 256 tile reads 1/8 fewer operand bytes per product than 256 x 192
+// (4096 x 2880 x 2880: 28.6 us, 256 x 192 33.8, and 31.7 with the ring as 3 x 256
+// instead of 6 x 128 K-elements).
+using I8Cfg = TileCfg<256, 6, 1, KIND_I8>;
 using I8GroupedCfg = TileCfg<256, 5, 1, KIND_I8>;   // the group table takes 4 KB of shared memory
-using I8NarrowCfg = TileCfg<64, 6, 1, KIND_I8>;
 
 __device__ unsigned int g_error_code;
 
@@ -346,24 +354,25 @@ __device__ __forceinline__ bool ragged_box(int64_t col, int width, int64_t ncols
 }
 
 // Backward epilogue, per warp: z boxes (32 rows x 64 columns, 4 KB) stream into
-// a ring of staging buffers by TMA, two boxes ahead of the one computed; each
-// box is replaced in place by dz and stored.  Buffer n % EPI_BUFS takes load n
-// once the store of load n - EPI_BUFS has read it: with two ahead, of the
-// stores committed so far all but the newest must have been read.  Boxes that
-// reach past their group's rows, and ragged ones, do not go through the ring.
+// a ring of staging buffers by TMA, EPI_BUFS - 2 boxes ahead of the one
+// computed; each box is replaced in place by dz and stored.  Buffer n % EPI_BUFS
+// takes load n once the store of load n - EPI_BUFS has read it: of the stores
+// committed so far all but the newest must have been read.  Boxes that reach
+// past their group's rows, and ragged ones, do not go through the ring.
 template <class Cfg, int MODE>
 struct ZRing {
     int t, j;                // next box to look at: pair tile, 32-column step
     uint32_t issued, used;
     TileInfo ti;
+    static constexpr uint32_t AHEAD = Cfg::EPI_BUFS - 2;
 
-    __device__ __forceinline__ void start(int t0) { t = t0; j = 0; issued = used = 0; }
-    // Issue loads until two boxes past the current one are in flight.
+    __device__ __forceinline__ void start(int t0, int part) { t = t0; j = part; issued = used = 0; }
+    // Issue loads until AHEAD boxes past the current one are in flight.
     __device__ __forceinline__ void fill(const CUtensorMap *map, uint8_t *bufs, uint64_t *bars, const GemmParams &p,
                                          const int *cum, int tiles_n, int ntiles, int npairs, uint32_t rank,
-                                         int row_lo, int lane) {
-        while (issued < used + 3 && t < ntiles) {
-            if (j == 0) ti = get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n);
+                                         int row_lo, int lane, int part) {
+        while (issued < used + AHEAD + 1 && t < ntiles) {
+            if (j == part) ti = get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n);
             const bool boxes = row_lo < ti.rows_valid && (MODE == MODE_DENSE || row_lo + 32 <= ti.rows_valid);
             const int64_t col0 = ti.n0 + 32 * j;
             if (boxes && col0 < p.N && !ragged_box(2 * col0, 64, 2 * p.N, 2)) {
@@ -375,7 +384,8 @@ struct ZRing {
                 }
                 ++issued;
             }
-            if (!boxes || ++j == Cfg::BN / 32) { j = 0; t += npairs; }
+            j += Cfg::SPLIT;
+            if (!boxes || j >= Cfg::BN / 32) { j = part; t += npairs; }
         }
         __syncwarp();
     }
@@ -457,7 +467,7 @@ __device__ __noinline__ void issue_stage_tail(uint32_t d_tmem, uint32_t st, uint
 }
 
 template <class Cfg, int MODE, int OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     mxfp4_gemm_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
                       const __grid_constant__ CUtensorMap tma_c, const __grid_constant__ CUtensorMap tma_sfa,
                       const __grid_constant__ CUtensorMap tma_sfb, const __grid_constant__ CUtensorMap tma_z,
@@ -472,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     Shared *sh = reinterpret_cast<Shared *>(epi_base + Cfg::EPI_BYTES);
     constexpr bool GROUPED = MODE == MODE_GROUPED_M;
     __shared__ int cum[MODE != MODE_DENSE ? MAX_GROUPS + 1 : 1];
-    __shared__ uint64_t zbar[OUT == OUT_GATED_BWD ? EPI_WARPS * Cfg::EPI_BUFS : 1];
+    __shared__ uint64_t zbar[OUT == OUT_GATED_BWD ? Cfg::EPI_WARPS * Cfg::EPI_BUFS : 1];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();               // 0 = MMA issuer of the pair
@@ -483,10 +493,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(&sh->full[s], 1); mbar_init(&sh->empty[s], 1); }
-        for (int b = 0; b < 2; ++b) { mbar_init(&sh->tmem_full[b], 1); mbar_init(&sh->tmem_empty[b], 2 * EPI_WARPS); }
+        for (int b = 0; b < 2; ++b) { mbar_init(&sh->tmem_full[b], 1); mbar_init(&sh->tmem_empty[b], 2 * Cfg::EPI_WARPS); }
         mbar_init(&sh->drain, 1);
         if constexpr (OUT == OUT_GATED_BWD)
-            for (int b = 0; b < EPI_WARPS * Cfg::EPI_BUFS; ++b) mbar_init(&zbar[b], 1);
+            for (int b = 0; b < Cfg::EPI_WARPS * Cfg::EPI_BUFS; ++b) mbar_init(&zbar[b], 1);
         sh->abort = 0;
         sh->drain_failed = 0;
         fence_barrier_init();
@@ -659,6 +669,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         // ------------------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3;                 // TMEM lane quarter of this warp
         const int ew = warp - 2;                // epilogue warp index
+        const int part = ew >> 2;               // which of the SPLIT warps of the quarter
+        int tile_i = 0;                         // tiles done by this CTA
         const uint32_t empty_leader0 = mapa_shared(smem_u32(&sh->tmem_empty[0]), 0);
         const uint32_t empty_leader1 = mapa_shared(smem_u32(&sh->tmem_empty[1]), 0);
         int acc = 0;
@@ -670,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         ZRing<Cfg, MODE> ring;
         uint8_t *ring_bufs = epi_base + ew * Cfg::EPI_BUFS * EPI_BUF;
         uint64_t *ring_bars = zbar + (OUT == OUT_GATED_BWD ? ew * Cfg::EPI_BUFS : 0);
-        ring.start(pair);
+        ring.start(pair, part);
         for (int t = pair; t < ntiles; t += npairs) {
             const TileInfo ti = get_tile<BN, MODE>(t, rank, p, cum, tiles_n);
             const int row_lo = 32 * q;
@@ -686,7 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 chan = load_chan(0);
             }
             if constexpr (OUT == OUT_GATED_BWD)
-                ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane);
+                ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
             if (!wait_phase(&sh->tmem_full[acc], acc_ph, sh, limit)) break;
             tc_fence_after();
             const bool full_box = MODE == MODE_DENSE || (row_lo + 32 <= ti.rows_valid);
@@ -742,23 +754,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 // 32 h (and the 64 z, if kept) leave as one box each
                 const GatedAct act{p.act_alpha, p.act_limit, p.act_beta};
                 const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16) + (acc ? Cfg::ACC1_COL : 0u);
-                for (int j = 0; j < BN / 64; ++j) {
+                // with two warps to a quarter, steps alternate over all tiles
+                // (three per tile: 2 and 1, then 1 and 2)
+                constexpr int NS = BN / 64;
+                const int first = Cfg::SPLIT == 1 ? 0 : ((tile_i * NS) & 1) ^ part;
+                const int last = Cfg::SPLIT == 1 ? NS - 1 : NS - 1 - ((NS - 1 - first) & 1);
+                for (int j = first; j < NS; j += Cfg::SPLIT) {
                     uint32_t w[32], hw[16];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t v[32];
                         tmem_ld_32x32b_x32(tm + 64u * j + 32u * h, v);
                         tmem_ld_wait();
+                        float hv[16];
+                        act.forward<16>(v, hv);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            hw[8 * h + i] = pack_bf16x2(
-                                act.forward(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
-                                act.forward(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+                        for (int i = 0; i < 8; ++i) hw[8 * h + i] = pack_bf16x2(hv[2 * i], hv[2 * i + 1]);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             w[16 * h + i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                     }
-                    if (j == BN / 64 - 1) {
+                    if (j == last) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
@@ -767,8 +783,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     if (!any_row || col0 >= p.N) continue;
                     if (full_box && !ragged_box(col0 >> 1, 32, p.N >> 1, 2)) {
                         for (int o = p.z ? 0 : 1; o < 2; ++o) {
-                            uint8_t *buf = epi_base + (ew * Cfg::EPI_BUFS + (buf_i & 1u)) * EPI_BUF;
-                            if (lane == 0) bulk_wait_group_read<1>();
+                            uint8_t *buf = epi_base + (ew * Cfg::EPI_BUFS + buf_i % Cfg::EPI_BUFS) * EPI_BUF;
+                            if (lane == 0) bulk_wait_group_read<Cfg::EPI_BUFS - 1>();
                             __syncwarp();
                             if (o == 0) stage_row128(smem_u32(buf), lane, w);
                             else stage_row64(smem_u32(buf), lane, hw);
@@ -792,11 +808,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 const GatedAct act{p.act_alpha, p.act_limit, p.act_beta};
                 const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16) + (acc ? Cfg::ACC1_COL : 0u);
                 bool ok = true;
-                for (int j = 0; j < BN / 32 && ok; ++j) {
+                for (int j = part; j < BN / 32; j += Cfg::SPLIT) {
                     uint32_t v[32], w[32];
                     tmem_ld_32x32b_x32(tm + 32u * j, v);
                     tmem_ld_wait();
-                    if (j == BN / 32 - 1) {
+                    if (j + Cfg::SPLIT >= BN / 32) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
@@ -809,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                     const uint32_t b = ring.used % Cfg::EPI_BUFS;
                     uint8_t *buf = ring_bufs + b * EPI_BUF;
                     if (in_ring) {
-                        ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane);
+                        ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
                         if (!wait_phase(&ring_bars[b], (ring.used / Cfg::EPI_BUFS) & 1u, sh, limit)) { ok = false; break; }
                         unstage_row128(smem_u32(buf), lane, w);
                     } else if (lane_row) {
@@ -818,8 +834,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = 0u;
                     }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) w[i] = act.backward(__uint_as_float(v[i]), w[i]);
+                    act.backward<16>(v, w);
+                    act.backward<16>(v + 16, w + 16);
                     if (in_ring) {
                         stage_row128(smem_u32(buf), lane, w);
                         fence_proxy_async_smem();
@@ -961,6 +977,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             if (++acc == 2) { acc = 0; acc_ph ^= 1u; }
+            ++tile_i;
         }
         if constexpr (OUT == OUT_GATED_BWD) {
             // after an abort: loads in flight land before the shared memory goes away
@@ -1156,7 +1173,7 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
         const int64_t tiles = (MODE == MODE_GROUPED_K ? g.G : 1) * ((g.M + 255) / 256) * ((g.N + BN - 1) / BN);
         pairs = (int)(tiles < pairs_max ? tiles : pairs_max);
     }
-    const cudaError_t e = launch_pdl(mxfp4_gemm_kernel<Cfg, MODE, OUT>, dim3((unsigned)(2 * pairs)), dim3(NUM_THREADS),
+    const cudaError_t e = launch_pdl(mxfp4_gemm_kernel<Cfg, MODE, OUT>, dim3((unsigned)(2 * pairs)), dim3(Cfg::THREADS),
                                      (size_t)Cfg::SMEM_BYTES, s, ta, tb, tc, tsa, tsb, tz, p);
     return e == cudaSuccess ? 0 : MXFP4_ERR_CUDA;
 }
@@ -1223,6 +1240,7 @@ int launch_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scal
 // Gated products: the activation of column pairs of A B^T (forward), or dz from
 // dh = A B^T and z (backward); offsets null for the dense forms.
 int launch_gated(const GatedArgs &a, cudaStream_t s) {
+    if (!a.offsets && !a.backward && gated_rows_fit(a.M, a.K)) return launch_gated_rows(a, s);
     GemmArgs g{a.a_codes, a.a_scales, a.b_codes, a.b_scales, a.lda, a.ldb, a.M, a.N, a.K, a.ld_out, a.out, a.offsets,
                a.sizes, a.offsets ? a.G : 1};
     g.z = a.z;
@@ -1233,11 +1251,12 @@ int launch_gated(const GatedArgs &a, cudaStream_t s) {
     if (a.backward)
         return a.offsets ? launch_cfg<BwdCfg, MODE_GROUPED_M, OUT_GATED_BWD>(g, s)
                          : launch_cfg<BwdCfg, MODE_DENSE, OUT_GATED_BWD>(g, s);
-    return a.offsets ? launch_cfg<DefaultCfg, MODE_GROUPED_M, OUT_GATED>(g, s)
-                     : launch_cfg<DefaultCfg, MODE_DENSE, OUT_GATED>(g, s);
+    return a.offsets ? launch_cfg<GatedCfg, MODE_GROUPED_M, OUT_GATED>(g, s)
+                     : launch_cfg<GatedCfg, MODE_DENSE, OUT_GATED>(g, s);
 }
 
 int launch_int8_gemm(const Int8Args &a, cudaStream_t s) {
+    if (!a.offsets && a.M <= ROWS_MAX) return launch_int8_rows(a, s);
     GemmArgs g{reinterpret_cast<const uint8_t *>(a.a), nullptr, reinterpret_cast<const uint8_t *>(a.b), nullptr, a.lda,
                a.ldb, a.M, a.N, a.K, a.ldc, a.c, a.offsets, a.sizes, a.offsets ? a.G : 1};
     g.a_tok = a.a_scales;

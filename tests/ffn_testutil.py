@@ -72,7 +72,7 @@ def int8_quantize(x32):
         amax = np.abs(x32).max(axis=1)
         ok = np.isfinite(amax)
         a = np.maximum(np.where(ok, amax, 1), np.float32(2.0 ** -100)).astype(np.float32)
-        inv = (np.float32(127.0) / a).astype(np.float32)
+        inv = ((np.float32(1.0) / a).astype(np.float32) * np.float32(127.0)).astype(np.float32)
         q = np.rint(np.where(ok[:, None], x32, 0) * inv[:, None]).astype(np.int8)
         scale = np.where(ok, (a / np.float32(127.0)).astype(np.float32), np.float32(np.nan))
     return q, scale.astype(np.float32)
