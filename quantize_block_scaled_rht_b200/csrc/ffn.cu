@@ -163,42 +163,89 @@ struct DropParams {
     void *y;
     int64_t rows, cols, ld_x, ld_r, ld_y;
     uint64_t block0;               // elem_offset / 4
-    uint32_t k0, k1, threshold;
-    int none;                      // p rounds to 1: nothing is kept
+    uint32_t k0, k1, last;         // dropped: words up to `last` = round(p 2^32) - 1
     float scale;
 };
 
+// ALL: round(p 2^32) is 0, every element is kept and no word is drawn.
+template <bool ALL>
 __device__ __forceinline__ float drop1(float x, uint32_t word, const DropParams &p) {
-    return word >= p.threshold && !p.none ? __fmul_rn(x, p.scale) : 0.0f;
+    return ALL || word > p.last ? __fmul_rn(x, p.scale) : 0.0f;
+}
+template <bool ALL>
+__device__ __forceinline__ U4 drop_words(uint64_t b, const DropParams &p) {
+    if constexpr (ALL) return U4{0, 0, 0, 0};
+    return philox4x32_10((uint32_t)b, (uint32_t)(b >> 32), 0u, DROPOUT_TAG, p.k0, p.k1);
 }
 
+// The same words with what depends on the counter's high half alone taken out of
+// the loop over blocks.  Counter words 2 and 3 are constant, so the first round
+// turns (lo, hi, 0, tag) into (hi ^ k0, 0, f(lo), g(lo)), and one of the second
+// round's two products is that of hi ^ k0.
+struct DropCounter {
+    uint32_t x, c3;                // of the second round: x = high half of M0 (hi ^ k0) ^ key, c3 = its low half
+
+    __device__ __forceinline__ void set(uint32_t hi, const DropParams &p) {
+        const uint64_t q = (uint64_t)0xD2511F53u * (hi ^ p.k0);
+        x = (uint32_t)(q >> 32) ^ (p.k1 + 0xBB67AE85u);
+        c3 = (uint32_t)q;
+    }
+    __device__ __forceinline__ U4 words(uint32_t lo, const DropParams &p) const {
+        const uint64_t a = (uint64_t)0xD2511F53u * lo;
+        const uint64_t b = (uint64_t)0xCD9E8D57u * ((uint32_t)(a >> 32) ^ (DROPOUT_TAG ^ p.k1));
+        return philox_rounds<2>((uint32_t)(b >> 32) ^ (p.k0 + 0x9E3779B9u), (uint32_t)b, (uint32_t)a ^ x, c3, p.k0, p.k1);
+    }
+};
+
 // A thread takes 16 bytes of a row (8 bf16 or 4 fp32) per step; cols is a
-// multiple of that, or there is one row with a tail.
-template <bool BF16, bool RES>
+// multiple of that, or there is one row with a tail.  FLAT: one row (contiguous
+// tensors), where a step's address is its index, whose blocks all have the same
+// high counter half (any tensor below 2^34 elements, but for an offset that
+// happens to cross a multiple of that).
+//
+// Bound by HBM with the residual or in FP32; plain bf16 by its integer
+// instructions, which all issue at one per two cycles: of about 116 per 8
+// elements Philox is 78.  65536 x 2880: 154 us (0.75 of HBM); with addresses
+// from row and column and every word from scratch 180; without drawing 118.
+template <bool BF16, bool RES, bool ALL, bool FLAT>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropParams p) {
     pdl_wait();
     pdl_trigger();
     constexpr int E = BF16 ? 8 : 4, SZ = BF16 ? 2 : 4;
-    const int64_t per_row = p.cols / E, n = p.rows * per_row;
+    const int64_t per_row = p.cols / E, n = FLAT ? per_row : p.rows * per_row;
     const char *x = static_cast<const char *>(p.x), *res = static_cast<const char *>(p.residual);
     char *y = static_cast<char *>(p.y);
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t row = p.rows == 1 ? 0 : i / per_row, c = (i - row * per_row) * E;
-        const uint4 u = ld_v4(x + (row * p.ld_x + c) * SZ);
+    DropCounter ctr;
+    if constexpr (FLAT && !ALL) ctr.set((uint32_t)(p.block0 >> 32), p);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        int64_t ox = 16 * i, orr = ox, oy = ox;
+        if constexpr (!FLAT) {
+            const int64_t row = i / per_row, c = (i - row * per_row) * E;
+            ox = (row * p.ld_x + c) * SZ;
+            oy = (row * p.ld_y + c) * SZ;
+            if constexpr (RES) orr = (row * p.ld_r + c) * SZ;
+        }
+        const uint4 u = ld_v4(x + ox);
         uint4 r = make_uint4(0, 0, 0, 0);
-        if constexpr (RES) r = ld_v4(res + (row * p.ld_r + c) * SZ);
+        if constexpr (RES) r = ld_v4(res + orr);
         const uint64_t b = p.block0 + (uint64_t)i * (E / 4);
-        const U4 w0 = philox4x32_10((uint32_t)b, (uint32_t)(b >> 32), 0u, DROPOUT_TAG, p.k0, p.k1);
+        U4 w0{}, w1{};
+        if constexpr (FLAT && !ALL) {
+            w0 = ctr.words((uint32_t)b, p);
+            if constexpr (BF16) w1 = ctr.words((uint32_t)b + 1u, p);
+        } else {
+            w0 = drop_words<ALL>(b, p);
+            if constexpr (BF16) w1 = drop_words<ALL>(b + 1, p);
+        }
         uint4 o;
         if constexpr (BF16) {
-            const U4 w1 = philox4x32_10((uint32_t)(b + 1), (uint32_t)((b + 1) >> 32), 0u, DROPOUT_TAG, p.k0, p.k1);
             const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
             float f[8], g[8];
             unpack_bf16x8(u, f);
             if constexpr (RES) unpack_bf16x8(r, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                f[e] = drop1(f[e], w[e], p);
+                f[e] = drop1<ALL>(f[e], w[e], p);
                 if constexpr (RES) f[e] = __fadd_rn(f[e], g[e]);
             }
             o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
@@ -209,18 +256,18 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropParams p) {
             const uint32_t w[4] = {w0.x, w0.y, w0.z, w0.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                f[e] = drop1(f[e], w[e], p);
+                f[e] = drop1<ALL>(f[e], w[e], p);
                 if constexpr (RES) f[e] = __fadd_rn(f[e], g[e]);
             }
             o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
         }
-        st_v4(y + (row * p.ld_y + c) * SZ, o);
+        st_v4(y + oy, o);
     }
 }
 
 // Any size, stride and alignment: a thread takes one Philox block, four
 // consecutive elements of the [rows, cols] order, from element `first` on.
-template <bool BF16, bool RES>
+template <bool BF16, bool RES, bool ALL>
 __global__ void __launch_bounds__(256) dropout_any_kernel(const DropParams p, int64_t first) {
     pdl_wait();
     pdl_trigger();
@@ -228,7 +275,7 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const DropParams p, in
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t e0 = first + 4 * i;
         const uint64_t b = p.block0 + (uint64_t)(e0 / 4);
-        const U4 w0 = philox4x32_10((uint32_t)b, (uint32_t)(b >> 32), 0u, DROPOUT_TAG, p.k0, p.k1);
+        const U4 w0 = drop_words<ALL>(b, p);
         const uint32_t w[4] = {w0.x, w0.y, w0.z, w0.w};
         int64_t row = e0 / p.cols, c = e0 - row * p.cols;
 #pragma unroll
@@ -236,12 +283,12 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const DropParams p, in
             if (e0 + e < total) {
                 if constexpr (BF16) {
                     const uint32_t v = static_cast<const uint16_t *>(p.x)[row * p.ld_x + c];
-                    float f = drop1(__uint_as_float(v << 16), w[e], p);
+                    float f = drop1<ALL>(__uint_as_float(v << 16), w[e], p);
                     if constexpr (RES)
                         f = __fadd_rn(f, __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.residual)[row * p.ld_r + c] << 16));
                     static_cast<uint16_t *>(p.y)[row * p.ld_y + c] = (uint16_t)pack_bf16x2(f, 0.0f);
                 } else {
-                    float f = drop1(static_cast<const float *>(p.x)[row * p.ld_x + c], w[e], p);
+                    float f = drop1<ALL>(static_cast<const float *>(p.x)[row * p.ld_x + c], w[e], p);
                     if constexpr (RES) f = __fadd_rn(f, static_cast<const float *>(p.residual)[row * p.ld_r + c]);
                     static_cast<float *>(p.y)[row * p.ld_y + c] = f;
                 }
@@ -251,7 +298,7 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const DropParams p, in
     }
 }
 
-template <bool BF16, bool RES>
+template <bool BF16, bool RES, bool ALL>
 cudaError_t run_dropout(DropParams p, cudaStream_t s) {
     constexpr int E = BF16 ? 8 : 4;
     auto al = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
@@ -271,12 +318,15 @@ cudaError_t run_dropout(DropParams p, cudaStream_t s) {
     if (aligned && (flat || strided)) {
         done = flat ? p.cols / E * E : p.rows * p.cols;
         if (done) {
-            const cudaError_t e = launch_pdl(dropout_kernel<BF16, RES>, grid(done / E), dim3(256), 0, s, p);
+            const bool one_hi = (p.block0 >> 32) == ((p.block0 + (uint64_t)(done / 4) - 1) >> 32);
+            const cudaError_t e = launch_pdl(flat && one_hi ? dropout_kernel<BF16, RES, ALL, true>
+                                                  : dropout_kernel<BF16, RES, ALL, false>,
+                                             grid(done / E), dim3(256), 0, s, p);
             if (e != cudaSuccess) return e;
         }
     }
     if (done == p.rows * p.cols) return cudaSuccess;
-    return launch_pdl(dropout_any_kernel<BF16, RES>, grid((p.rows * p.cols - done + 3) / 4), dim3(256), 0, s, p, done);
+    return launch_pdl(dropout_any_kernel<BF16, RES, ALL>, grid((p.rows * p.cols - done + 3) / 4), dim3(256), 0, s, p, done);
 }
 
 }  // namespace
@@ -284,12 +334,15 @@ cudaError_t run_dropout(DropParams p, cudaStream_t s) {
 cudaError_t launch_dropout(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, int64_t rows,
                            int64_t cols, int dtype, double prob, uint64_t seed, uint64_t elem_offset, void *y,
                            int64_t ld_y, cudaStream_t s) {
-    const double t = std::nearbyint(prob * 4294967296.0);
-    DropParams p{x, residual, y, rows, cols, ld_x, ld_residual, ld_y, elem_offset / 4, (uint32_t)seed,
-                 (uint32_t)(seed >> 32), t >= 4294967296.0 ? 0u : (uint32_t)t, t >= 4294967296.0,
-                 prob < 1.0 ? (float)(1.0 / (1.0 - prob)) : 0.0f};
-    if (dtype == MXFP4_OUT_BF16) return residual ? run_dropout<true, true>(p, s) : run_dropout<true, false>(p, s);
-    return residual ? run_dropout<false, true>(p, s) : run_dropout<false, false>(p, s);
+    const double t = std::nearbyint(prob * 4294967296.0);   // 0 .. 2^32
+    const DropParams p{x, residual, y, rows, cols, ld_x, ld_residual, ld_y, elem_offset / 4, (uint32_t)seed,
+                       (uint32_t)(seed >> 32), t > 0.0 ? (uint32_t)(t - 1.0) : 0u, prob < 1.0 ? (float)(1.0 / (1.0 - prob)) : 0.0f};
+    const bool bf16 = dtype == MXFP4_OUT_BF16, res = residual != nullptr;
+    if (t == 0.0)
+        return bf16 ? (res ? run_dropout<true, true, true>(p, s) : run_dropout<true, false, true>(p, s))
+                    : (res ? run_dropout<false, true, true>(p, s) : run_dropout<false, false, true>(p, s));
+    return bf16 ? (res ? run_dropout<true, true, false>(p, s) : run_dropout<true, false, false>(p, s))
+                : (res ? run_dropout<false, true, false>(p, s) : run_dropout<false, false, false>(p, s));
 }
 
 }  // namespace mxfp4
