@@ -564,16 +564,16 @@ def _run(fn, what: str, idx: int, stream, *args) -> None:
         raise MXFP4Error(rc, what)
 
 
-def _device(what: str, stream, *ts: torch.Tensor) -> int:
+def _device(what: str, stream, t: torch.Tensor, *others: torch.Tensor) -> int:
     """Index of the one CUDA device of the tensors, checked against the stream's."""
-    idx = ts[0].get_device()
-    for t in ts:
-        if t.get_device() != idx:
-            raise ValueError(f"{what}: tensors on different devices: {ts[0].device} and {t.device}")
+    idx = t.get_device()
     if idx < 0:
         raise ValueError("libmxfp4 takes CUDA tensors (device pointers)")
+    for o in others:
+        if o.get_device() != idx:
+            raise ValueError(f"{what}: tensors on different devices: {t.device} and {o.device}")
     if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device.index != idx:
-        raise ValueError(f"{what}: stream of {stream.device} for tensors on {ts[0].device}")
+        raise ValueError(f"{what}: stream of {stream.device} for tensors on {t.device}")
     return idx
 
 
@@ -597,19 +597,25 @@ def _empty_rows(rows: int, cols: int, dtype: torch.dtype, idx: int, stream):
     return _empty((rows, ld), dtype, idx, stream)[:, :cols], ld
 
 
-def _rows(t: torch.Tensor, what: str, dtypes: tuple, shape=None) -> int:
-    """Checks a 2-D row-major tensor of one of these types (and this shape);
-    returns its row stride.  A single row's stride is never used, and torch may
-    leave any: it stands at a 16-byte multiple that covers the row."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    got = t.shape
-    if len(got) != 2 or (shape is not None and got != shape):
-        raise ValueError(f"{what} must be a row-major tensor of shape {tuple(shape or ('rows', 'columns'))}, got {tuple(got)}")
+def _rows(t: torch.Tensor, what: str, *dtypes: torch.dtype) -> tuple:
+    """(rows, columns, row stride) of a 2-D row-major tensor of one of these types.
+    A single row's stride is never used, and torch may leave any: it stands at a
+    16-byte multiple that covers the row."""
+    if t.dtype not in dtypes or t.dim() != 2:
+        raise ValueError(f"{what} must be a row-major 2-D tensor of {' or '.join(map(str, dtypes))}, got {t.dim()}-D {t.dtype}")
+    rows, cols = t.shape
     ld, step = t.stride()
-    if step != 1 and got[1] > 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{what} must be row-major, got strides {t.stride()}")
-    return ld if got[0] > 1 else (got[1] + 15) // 16 * 16
+    return rows, cols, ld if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _rows_of(t: torch.Tensor, what: str, dtype: torch.dtype, rows: int, cols: int) -> int:
+    """Row stride of a tensor that has to have this type and shape."""
+    r, c, ld = _rows(t, what, dtype)
+    if r != rows or c != cols:
+        raise ValueError(f"{what} must be of shape {(rows, cols)}, got {(r, c)}")
+    return ld
 
 
 def _groups(what: str, offsets: torch.Tensor, sizes: torch.Tensor, b: torch.Tensor) -> int:
@@ -625,15 +631,14 @@ def _groups(what: str, offsets: torch.Tensor, sizes: torch.Tensor, b: torch.Tens
     return G
 
 
-def _b_rows(b: torch.Tensor, what: str, dtype: torch.dtype, grouped: bool) -> int:
-    """Checks B, [N, K] or [G, N, K] codes with contiguous rows; returns its row stride."""
-    if b.dtype != dtype:
-        raise ValueError(f"{what}: codes must be {dtype} tensors")
-    if b.dim() != (3 if grouped else 2) or b.stride(-1) != 1:
-        raise ValueError(f"{what}: B must be row-major codes {'[G, N, K]' if grouped else '[N, K]'}, got {tuple(b.shape)} "
-                         f"with strides {b.stride()}")
-    ld = b.stride(-2)
-    return ld if grouped or b.shape[0] > 1 else (b.shape[1] + 15) // 16 * 16
+def _b_rows(b: torch.Tensor, what: str, dtype: torch.dtype, grouped: bool) -> tuple:
+    """(N, bytes per row, row stride) of B, codes [N, K] or [G, N, K] with contiguous rows."""
+    if not grouped:
+        return _rows(b, "B", dtype)
+    if b.dtype is not dtype or b.dim() != 3 or b.stride(2) != 1:
+        raise ValueError(f"{what}: B must be row-major {dtype} codes [G, N, K], got {b.dtype} {tuple(b.shape)} with strides "
+                         f"{b.stride()}")
+    return b.shape[1], b.shape[2], b.stride(1)
 
 
 def _scales_ready(t: torch.Tensor, name: str, what: str, rows: int, K: int, groups: int = 1) -> int:
@@ -646,40 +651,42 @@ def _scales_ready(t: torch.Tensor, name: str, what: str, rows: int, K: int, grou
     return t.data_ptr()
 
 
-_U8, _I8, _BF16, _BF16_F32 = (torch.uint8,), (torch.int8,), (torch.bfloat16,), (torch.bfloat16, torch.float32)
-
-
 def _gated(name: str, a_codes, a_scales, groups, b_codes, b_scales, K, alpha, limit, beta, z, keep_z, out, stream):
     """The four gated entry points: z None or a tensor to write (forward), or the
     kept pre-activations (backward: keep_z is None)."""
     grouped, backward = groups is not None, keep_z is None
-    lda = _rows(a_codes, "A", _U8)
-    ldb = _b_rows(b_codes, name, torch.uint8, grouped)
-    (M, ka), (N, kb) = a_codes.shape, b_codes.shape[-2:]
+    M, ka, lda = _rows(a_codes, "A", torch.uint8)
+    N, kb, ldb = _b_rows(b_codes, name, torch.uint8, grouped)
     if 2 * ka < K or 2 * kb < K:
         raise ValueError(f"{name}: codes hold {2 * min(ka, kb)} elements per row, K = {K}")
     G = _groups(name, *groups, b_codes) if grouped else 1
-    first = (a_codes.data_ptr(), lda, _scales_ready(a_scales, name, "a_scales", M, K))
-    second = (b_codes.data_ptr(), ldb, _scales_ready(b_scales, name, "b_scales", N, K, G))
+    psa = _scales_ready(a_scales, name, "a_scales", M, K)
+    psb = _scales_ready(b_scales, name, "b_scales", N, K, G)
     if not backward and N % 2:
         raise ValueError(f"{name}: B holds gate and up rows in turn, N = {N} is odd")
     ocols, zcols = (2 * N, 2 * N) if backward else (N // 2, N)
-    used = [a_codes, a_scales, b_codes, b_scales, *(groups or ())]
+    pz, ldz = None, 0
     if z is not None:
-        ldz = _rows(z, "z", _BF16, (M, zcols))
-        used.append(z)
+        pz, ldz = z.data_ptr(), _rows_of(z, "z", torch.bfloat16, M, zcols)
+        _device(name, stream, a_codes, z)
     if out is not None:
-        ldo = _rows(out, "out", _BF16, (M, ocols))
-        used.append(out)
-    idx = _device(name, stream, *used)
+        ldo = _rows_of(out, "out", torch.bfloat16, M, ocols)
+        _device(name, stream, a_codes, out)
+    idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales)
     if out is None:
         out, ldo = _empty_rows(M, ocols, torch.bfloat16, idx, stream)
     if keep_z and z is None:
         z, ldz = _empty_rows(M, zcols, torch.bfloat16, idx, stream)
-    rows = (M, groups[0].data_ptr(), groups[1].data_ptr(), G, *second, N, K) if grouped else (*second, M, N, K)
-    pz, po = (None, 0) if z is None else (z.data_ptr(), ldz), (out.data_ptr(), ldo)
-    _run(getattr(_lib or lib(), name), name, idx, stream, *first, *rows, alpha, limit, beta,
-         *(pz + po if backward else po + pz))
+        pz = z.data_ptr()
+    act_and_out = (alpha, limit, beta, pz, ldz, out.data_ptr(), ldo) if backward else \
+        (alpha, limit, beta, out.data_ptr(), ldo, pz, ldz)
+    fn = getattr(_lib or lib(), name)
+    if grouped:
+        _device(name, stream, a_codes, *groups)
+        _run(fn, name, idx, stream, a_codes.data_ptr(), lda, psa, M, groups[0].data_ptr(), groups[1].data_ptr(), G,
+             b_codes.data_ptr(), ldb, psb, N, K, *act_and_out)
+    else:
+        _run(fn, name, idx, stream, a_codes.data_ptr(), lda, psa, b_codes.data_ptr(), ldb, psb, M, N, K, *act_and_out)
     return out, z
 
 
@@ -739,15 +746,14 @@ def mxfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Quantized] = None, st
     """Signed 8-bit codes and one scale per row of a 2-D bf16 tensor: activations
     by token, a weight [N, K] by output channel (see mxfp4_int8_quantize in
     include/mxfp4.h)."""
-    ld = _rows(x, "x", _BF16)
-    rows, cols = x.shape
+    rows, cols, ld = _rows(x, "x", torch.bfloat16)
     if out is None:
         idx = _device("mxfp4_int8_quantize", stream, x)
         codes, scales = _empty((rows, cols), torch.int8, idx, stream), _empty((rows,), torch.float32, idx, stream)
         ldc, out = cols, Int8Quantized(codes, scales)
     else:
         codes, scales = out.codes, out.scales
-        ldc = _rows(codes, "out.codes", _I8, (rows, cols))
+        ldc = _rows_of(codes, "out.codes", torch.int8, rows, cols)
         _token_scales(scales, "out.scales", (rows,))
         idx = _device("mxfp4_int8_quantize", stream, x, codes, scales)
     _run((_lib or lib()).mxfp4_int8_quantize, "mxfp4_int8_quantize", idx, stream, x.data_ptr(), rows, cols, ld,
@@ -763,25 +769,32 @@ def _token_scales(t: torch.Tensor, what: str, shape: tuple) -> int:
 
 def _int8_gemm(name: str, a_codes, a_scales, groups, b_codes, b_scales, out_dtype, out, stream) -> torch.Tensor:
     grouped = groups is not None
-    lda = _rows(a_codes, "A", _I8)
-    ldb = _b_rows(b_codes, name, torch.int8, grouped)
-    (M, K), (N, kb) = a_codes.shape, b_codes.shape[-2:]
+    M, K, lda = _rows(a_codes, "A", torch.int8)
+    N, kb, ldb = _b_rows(b_codes, name, torch.int8, grouped)
     if kb != K:
         raise ValueError(f"{name}: A has K = {K}, B {kb}")
     G = _groups(name, *groups, b_codes) if grouped else 1
-    first = (a_codes.data_ptr(), lda, _token_scales(a_scales, "a_scales", (M,)))
-    second = (b_codes.data_ptr(), ldb, _token_scales(b_scales, "b_scales", (G, N) if grouped else (N,)))
+    psa = _token_scales(a_scales, "a_scales", (M,))
+    psb = _token_scales(b_scales, "b_scales", (G, N) if grouped else (N,))
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError(f"{name}: the output must be bfloat16 or float32, got out_dtype {out_dtype}")
     if out is None:
-        if out_dtype not in _BF16_F32:
-            raise ValueError(f"{name}: out_dtype must be bfloat16 or float32")
-        idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales, *(groups or ()))
+        idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales)
         out, ldo = _empty_rows(M, N, out_dtype, idx, stream)
     else:
-        ldo = _rows(out, "out", _BF16_F32, (M, N))
-        idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales, out, *(groups or ()))
-    rows = (M, groups[0].data_ptr(), groups[1].data_ptr(), G, *second, N, K) if grouped else (*second, M, N, K)
-    _run(getattr(_lib or lib(), name), name, idx, stream, *first, *rows, out.data_ptr(), ldo,
-         OUT_F32 if out.dtype == torch.float32 else OUT_BF16)
+        ldo = _rows_of(out, "out", out_dtype, M, N)
+        idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales, out)
+    kind = OUT_F32 if out_dtype is torch.float32 else OUT_BF16
+    fn = getattr(_lib or lib(), name)
+    if grouped:
+        _device(name, stream, a_codes, *groups)
+        _run(fn, name, idx, stream, a_codes.data_ptr(), lda, psa, M, groups[0].data_ptr(), groups[1].data_ptr(), G,
+             b_codes.data_ptr(), ldb, psb, N, K, out.data_ptr(), ldo, kind)
+    else:
+        _run(fn, name, idx, stream, a_codes.data_ptr(), lda, psa, b_codes.data_ptr(), ldb, psb, M, N, K, out.data_ptr(), ldo,
+             kind)
     return out
 
 
@@ -810,22 +823,22 @@ def mxfp4_dropout(x: torch.Tensor, p: float, seed: int, elem_offset: int = 0, re
     from the Philox stream of (seed, element index) and never stored (see
     mxfp4_dropout in include/mxfp4.h).  The gradient is the same call on dY.
     out may be x or residual itself."""
-    ld = _rows(x, "x", _BF16_F32)
-    kind, shape, res = (x.dtype,), x.shape, (None, 0)
-    used = [x]
-    if residual is not None:
-        res = (residual.data_ptr(), _rows(residual, "residual", kind, shape))
-        used.append(residual)
-    if out is not None:
-        ldo = _rows(out, "out", kind, shape)
-        used.append(out)
+    rows, cols, ld = _rows(x, "x", torch.bfloat16, torch.float32)
+    kind = x.dtype
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be within [0, 1], got {p}")
-    idx = _device("mxfp4_dropout", stream, *used)
+    pr, ldr = None, 0
+    if residual is not None:
+        pr, ldr = residual.data_ptr(), _rows_of(residual, "residual", kind, rows, cols)
+        _device("mxfp4_dropout", stream, x, residual)
+    idx = _device("mxfp4_dropout", stream, x)
     if out is None:
-        out, ldo = _empty(shape, x.dtype, idx, stream), shape[1]
-    _run((_lib or lib()).mxfp4_dropout, "mxfp4_dropout", idx, stream, x.data_ptr(), ld, *res, shape[0], shape[1],
-         OUT_F32 if x.dtype == torch.float32 else OUT_BF16, p, seed & 0xFFFFFFFFFFFFFFFF, elem_offset, out.data_ptr(), ldo)
+        out, ldo = _empty((rows, cols), kind, idx, stream), cols
+    else:
+        ldo = _rows_of(out, "out", kind, rows, cols)
+        _device("mxfp4_dropout", stream, x, out)
+    _run((_lib or lib()).mxfp4_dropout, "mxfp4_dropout", idx, stream, x.data_ptr(), ld, pr, ldr, rows, cols,
+         OUT_F32 if kind is torch.float32 else OUT_BF16, p, seed & 0xFFFFFFFFFFFFFFFF, elem_offset, out.data_ptr(), ldo)
     return out
 
 

@@ -126,11 +126,20 @@ using NvCfg = TileCfg<192, 5, 1, KIND_NV>;
 // a ring of 5 x 256 43.3).
 using GatedCfg = TileCfg<192, 3, 2, KIND_MX, 1, 8>;
 using BwdCfg = TileCfg<192, 4, 1, KIND_MX, 3, 8>;
+// Dense calls take 128-column tiles where those finish in clearly fewer rounds
+// of tiles (launch_dense): 256 x 5760 x 2880 8.0 against 9.1 us, 768 rows 11.5
+// against 13.0; backward, 768 x 2880 x 2880, 12.4 against 14.1.
+using GatedNarrowCfg = TileCfg<128, 3, 2, KIND_MX, 2, 8>;
+using BwdNarrowCfg = TileCfg<128, 4, 1, KIND_MX, 3, 8>;
 // int8: without scale factors in tensor memory two 256-column accumulators fit,
 // and a 256 x 256 tile reads 1/8 fewer operand bytes per product than 256 x 192
 // (4096 x 2880 x 2880: 28.6 us, 256 x 192 33.8, and 31.7 with the ring as 3 x 256
 // instead of 6 x 128 K-elements).
+// Narrow: 128 x 2880 x 2880 10.2 against 12.6 us, 64 x 8192 x 8192 19.8 against
+// 24.4; where it would take two rounds to the wide tile's one, the fewer operand
+// bytes win (1024 x 2880 x 2880: 13.8 against 16.4).
 using I8Cfg = TileCfg<256, 6, 1, KIND_I8>;
+using I8NarrowCfg = TileCfg<128, 8, 1, KIND_I8>;
 using I8GroupedCfg = TileCfg<256, 5, 1, KIND_I8>;   // the group table takes 4 KB of shared memory
 
 __device__ unsigned int g_error_code;
@@ -1237,6 +1246,17 @@ int launch_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scal
     return launch_cfg<NvCfg, MODE_DENSE>(g, s);
 }
 
+// Dense launch with the wide or the narrow tile: a narrow tile costs 0.65 to 0.8
+// of a wide one (its instructions are shorter, its operand bytes per product
+// more), so it has to save that much in rounds of the resident pairs.
+template <class Wide, class Narrow, int OUT>
+static int launch_dense(const GemmArgs &g, cudaStream_t s) {
+    const int64_t pairs = sm_count() / 2, tiles_m = (g.M + 255) / 256;
+    auto rounds = [&](int64_t bn) { return (tiles_m * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
+    if (4 * rounds(Narrow::BN) < 5 * rounds(Wide::BN)) return launch_cfg<Narrow, MODE_DENSE, OUT>(g, s);
+    return launch_cfg<Wide, MODE_DENSE, OUT>(g, s);
+}
+
 // Gated products: the activation of column pairs of A B^T (forward), or dz from
 // dh = A B^T and z (backward); offsets null for the dense forms.
 int launch_gated(const GatedArgs &a, cudaStream_t s) {
@@ -1250,9 +1270,9 @@ int launch_gated(const GatedArgs &a, cudaStream_t s) {
     g.beta = a.beta;
     if (a.backward)
         return a.offsets ? launch_cfg<BwdCfg, MODE_GROUPED_M, OUT_GATED_BWD>(g, s)
-                         : launch_cfg<BwdCfg, MODE_DENSE, OUT_GATED_BWD>(g, s);
+                         : launch_dense<BwdCfg, BwdNarrowCfg, OUT_GATED_BWD>(g, s);
     return a.offsets ? launch_cfg<GatedCfg, MODE_GROUPED_M, OUT_GATED>(g, s)
-                     : launch_cfg<GatedCfg, MODE_DENSE, OUT_GATED>(g, s);
+                     : launch_dense<GatedCfg, GatedNarrowCfg, OUT_GATED>(g, s);
 }
 
 int launch_int8_gemm(const Int8Args &a, cudaStream_t s) {
@@ -1264,7 +1284,7 @@ int launch_int8_gemm(const Int8Args &a, cudaStream_t s) {
     if (a.offsets)
         return a.bf16 ? launch_cfg<I8GroupedCfg, MODE_GROUPED_M, OUT_BF16>(g, s)
                       : launch_cfg<I8GroupedCfg, MODE_GROUPED_M, OUT_F32>(g, s);
-    return a.bf16 ? launch_cfg<I8Cfg, MODE_DENSE, OUT_BF16>(g, s) : launch_cfg<I8Cfg, MODE_DENSE, OUT_F32>(g, s);
+    return a.bf16 ? launch_dense<I8Cfg, I8NarrowCfg, OUT_BF16>(g, s) : launch_dense<I8Cfg, I8NarrowCfg, OUT_F32>(g, s);
 }
 
 int get_error(cudaStream_t s) {

@@ -58,7 +58,8 @@ def no_error():
 
 # ------------------------------------------------------------------ gated product
 FWD = [(1, 8, 64), (2, 96, 128), (3, 1000, 64), (7, 40, 2880), (8, 96, 4160), (9, 96, 128), (37, 48, 192), (128, 96, 512), (130, 104, 320),
-       (300, 200, 2880), (257, 500, 576), (513, 64, 64)]
+       (300, 200, 2880), (257, 500, 576), (513, 64, 64),
+       (1100, 2500, 128), (2600, 700, 320)]
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -179,7 +180,7 @@ def z_values(rows, I, seed):
 
 
 BWD = [(1, 8, 64), (5, 40, 128), (128, 96, 512), (130, 104, 320), (300, 200, 2880), (257, 500, 576), (64, 1600, 64),
-       (1000, 260, 192)]
+       (1000, 260, 192), (1300, 2180, 128), (2600, 1004, 576)]
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -335,7 +336,7 @@ def test_int8_quantize_every_bf16_value_and_strides():
 # ------------------------------------------------------------------ int8 product
 I8_SHAPES = [(1, 8, 16), (1, 200, 2880), (2, 13, 48), (4, 64, 5760), (5, 260, 144), (8, 512, 1040), (9, 40, 272), (16, 300, 512),
              (17, 256, 256), (64, 96, 2880), (129, 257, 528), (256, 256, 256), (300, 1000, 208), (513, 72, 4112),
-             (40, 48, 240), (2, 72, 112), (100, 24, 496)]
+             (40, 48, 240), (2, 72, 112), (100, 24, 496), (1100, 2700, 208), (5000, 600, 272)]
 
 
 def int8_operands(M, N, K, seed, G=None):
