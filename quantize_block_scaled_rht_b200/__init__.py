@@ -577,24 +577,22 @@ def _device(what: str, stream, t: torch.Tensor, *others: torch.Tensor) -> int:
     return idx
 
 
-def _empty(shape, dtype: torch.dtype, idx: int, stream) -> torch.Tensor:
+def _empty(shape: tuple, strides: tuple, dtype: torch.dtype, idx: int, stream) -> torch.Tensor:
     """An output tensor that belongs to the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=idx)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=idx)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=idx)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=idx)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=idx)
 
 
 def _empty_rows(rows: int, cols: int, dtype: torch.dtype, idx: int, stream):
-    """(_empty, its row stride) with rows that start on 16-byte boundaries, as the
-    kernels store them: a view of a wider tensor where cols alone does not give that."""
+    """(tensor, its row stride): rows start on 16-byte boundaries, as the kernels
+    store them, so the stride is above cols where cols alone does not give that."""
     per = 8 if dtype is torch.bfloat16 else 4
-    if not cols % per:
-        return _empty((rows, cols), dtype, idx, stream), cols
     ld = (cols + per - 1) // per * per
-    return _empty((rows, ld), dtype, idx, stream)[:, :cols], ld
+    return _empty((rows, cols), (ld, 1), dtype, idx, stream), ld
 
 
 def _rows(t: torch.Tensor, what: str, *dtypes: torch.dtype) -> tuple:
@@ -749,7 +747,8 @@ def mxfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Quantized] = None, st
     rows, cols, ld = _rows(x, "x", torch.bfloat16)
     if out is None:
         idx = _device("mxfp4_int8_quantize", stream, x)
-        codes, scales = _empty((rows, cols), torch.int8, idx, stream), _empty((rows,), torch.float32, idx, stream)
+        codes = _empty((rows, cols), (cols, 1), torch.int8, idx, stream)
+        scales = _empty((rows,), (1,), torch.float32, idx, stream)
         ldc, out = cols, Int8Quantized(codes, scales)
     else:
         codes, scales = out.codes, out.scales
@@ -833,7 +832,7 @@ def mxfp4_dropout(x: torch.Tensor, p: float, seed: int, elem_offset: int = 0, re
         _device("mxfp4_dropout", stream, x, residual)
     idx = _device("mxfp4_dropout", stream, x)
     if out is None:
-        out, ldo = _empty((rows, cols), kind, idx, stream), cols
+        out, ldo = _empty((rows, cols), (cols, 1), kind, idx, stream), cols
     else:
         ldo = _rows_of(out, "out", kind, rows, cols)
         _device("mxfp4_dropout", stream, x, out)
