@@ -29,16 +29,22 @@ struct GatedAct {
     // values at a time: a warp of the GEMM's epilogue has a scheduler to itself,
     // so only independent values hide the latency of a step.
     template <int N>
-    __device__ __forceinline__ void sigmoid(const float *g, float *s) const {
+    __device__ __forceinline__ void sigmoid(const float2 *g, float2 *s) const {
         const float k = __fmul_rn(alpha, -1.44269504f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = __fmul_rn(g[i], k);
+        for (int i = 0; i < N; ++i) s[i] = mul2(g[i], make_float2(k, k));
 #pragma unroll
-        for (int i = 0; i < N; ++i) asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
+        for (int i = 0; i < N; ++i) {
+            asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[i].x));
+            asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[i].y));
+        }
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = __fadd_rn(s[i], 1.0f);
+        for (int i = 0; i < N; ++i) s[i] = add2(s[i], make_float2(1.0f, 1.0f));
 #pragma unroll
-        for (int i = 0; i < N; ++i) asm volatile("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[i]));
+        for (int i = 0; i < N; ++i) {
+            asm volatile("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[i].x));
+            asm volatile("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[i].y));
+        }
     }
     // One instruction per bound; a NaN goes through.
     __device__ __forceinline__ float clamp_gate(float z) const {
@@ -51,33 +57,39 @@ struct GatedAct {
         asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(clamp_gate(z)), "f"(-limit));
         return r;
     }
-    // N pairs (zg, zu) in v, FP32 bits, to N values h.
+    // 2N pairs (zg, zu) in v, FP32 bits, to 2N values h, two at a time in packed
+    // FP32 (each lane rounded as the scalar operation, half the issue slots).
     template <int N>
-    __device__ __forceinline__ void forward(const uint32_t *v, float *h) const {
-        float s[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) h[i] = clamp_gate(__uint_as_float(v[2 * i]));
-        sigmoid<N>(h, s);
+    __device__ __forceinline__ void forward(const uint32_t *v, float2 *h) const {
+        float2 s[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            h[i] = __fmul_rn(__fmul_rn(h[i], s[i]), __fadd_rn(clamp_up(__uint_as_float(v[2 * i + 1])), beta));
+            h[i] = make_float2(clamp_gate(__uint_as_float(v[4 * i])), clamp_gate(__uint_as_float(v[4 * i + 2])));
+        sigmoid<N>(h, s);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 u = make_float2(clamp_up(__uint_as_float(v[4 * i + 1])), clamp_up(__uint_as_float(v[4 * i + 3])));
+            h[i] = mul2(mul2(h[i], s[i]), add2(u, make_float2(beta, beta)));
+        }
     }
-    // N values dh (FP32 bits) and packed bf16 pairs z (zg low, zu high), the
+    // 2N values dh (FP32 bits) and packed bf16 pairs z (zg low, zu high), the
     // pairs replaced by (dzg, dzu).
     template <int N>
     __device__ __forceinline__ void backward(const uint32_t *dh, uint32_t *z) const {
-        float g[N], s[N];
+        float2 g[N], s[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = clamp_gate(bf16lo(z[i]));
+        for (int i = 0; i < N; ++i) g[i] = make_float2(clamp_gate(bf16lo(z[2 * i])), clamp_gate(bf16lo(z[2 * i + 1])));
         sigmoid<N>(g, s);
+        const float2 a = make_float2(alpha, alpha), b = make_float2(beta, beta), one = make_float2(1.0f, 1.0f);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float zu = bf16hi(z[i]);
-            const float t = __fmaf_rn(__fmul_rn(alpha, g[i]), __fsub_rn(1.0f, s[i]), 1.0f);
-            const float hs = __fmul_rn(__uint_as_float(dh[i]), s[i]);
-            const float dg = __fmul_rn(__fmul_rn(hs, __fadd_rn(clamp_up(zu), beta)), t);
-            const float du = __fmul_rn(hs, g[i]);
-            z[i] = pack_bf16x2(bf16lo(z[i]) > limit ? 0.0f : dg, fabsf(zu) > limit ? 0.0f : du);
+            const uint32_t z0 = z[2 * i], z1 = z[2 * i + 1];
+            const float2 u = make_float2(clamp_up(bf16hi(z0)), clamp_up(bf16hi(z1)));
+            const float2 t = fma2(mul2(a, g[i]), sub2(one, s[i]), one);
+            const float2 hs = mul2(make_float2(__uint_as_float(dh[2 * i]), __uint_as_float(dh[2 * i + 1])), s[i]);
+            const float2 dg = mul2(mul2(hs, add2(u, b)), t), du = mul2(hs, g[i]);
+            z[2 * i] = pack_bf16x2(bf16lo(z0) > limit ? 0.0f : dg.x, fabsf(bf16hi(z0)) > limit ? 0.0f : du.x);
+            z[2 * i + 1] = pack_bf16x2(bf16lo(z1) > limit ? 0.0f : dg.y, fabsf(bf16hi(z1)) > limit ? 0.0f : du.y);
         }
     }
 };

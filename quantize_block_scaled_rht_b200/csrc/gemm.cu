@@ -123,7 +123,7 @@ using NvCfg = TileCfg<192, 5, 1, KIND_NV>;
 // product's time; 4 warps and two buffers 48.8, 8 warps and two buffers on a
 // ring of 5 x 256 40.2).  Backward: three buffers carry z in and dz out, paid for
 // with a ring of 4 x 256 (4096 x 2880 x 2880: 38.3 us; 4 warps, four buffers and
-// a ring of 5 x 256 43.3).
+// a ring of 5 x 256 43.3; packed FP32 and z read beside the accumulators 36.8).
 using GatedCfg = TileCfg<192, 3, 2, KIND_MX, 1, 8>;
 using BwdCfg = TileCfg<192, 4, 1, KIND_MX, 3, 8>;
 // Dense calls take 128-column tiles where those finish in clearly fewer rounds
@@ -775,10 +775,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                         uint32_t v[32];
                         tmem_ld_32x32b_x32(tm + 64u * j + 32u * h, v);
                         tmem_ld_wait();
-                        float hv[16];
-                        act.forward<16>(v, hv);
+                        float2 hv[8];
+                        act.forward<8>(v, hv);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) hw[8 * h + i] = pack_bf16x2(hv[2 * i], hv[2 * i + 1]);
+                        for (int i = 0; i < 8; ++i) hw[8 * h + i] = pack_bf16x2(hv[i].x, hv[i].y);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             w[16 * h + i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
@@ -820,31 +820,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 for (int j = part; j < BN / 32; j += Cfg::SPLIT) {
                     uint32_t v[32], w[32];
                     tmem_ld_32x32b_x32(tm + 32u * j, v);
-                    tmem_ld_wait();
-                    if (j + Cfg::SPLIT >= BN / 32) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
-                    }
+                    // z arrives while the accumulators do
                     const int64_t col0 = ti.n0 + 32 * j;
-                    if (!any_row || col0 >= p.N) continue;
+                    const bool used = any_row && col0 < p.N;
                     const int64_t row = ti.c_row0 + row_lo + lane, zleft = 2 * (p.N - col0);
-                    const bool lane_row = row_lo + lane < ti.rows_valid;
-                    const bool in_ring = full_box && !ragged_box(2 * col0, 64, 2 * p.N, 2);
+                    const bool lane_row = used && row_lo + lane < ti.rows_valid;
+                    const bool in_ring = used && full_box && !ragged_box(2 * col0, 64, 2 * p.N, 2);
                     const uint32_t b = ring.used % Cfg::EPI_BUFS;
                     uint8_t *buf = ring_bufs + b * EPI_BUF;
                     if (in_ring) {
                         ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
-                        if (!wait_phase(&ring_bars[b], (ring.used / Cfg::EPI_BUFS) & 1u, sh, limit)) { ok = false; break; }
-                        unstage_row128(smem_u32(buf), lane, w);
+                        // one answer for the warp: the tensor memory instructions need it whole
+                        ok = __all_sync(0xFFFFFFFFu, wait_phase(&ring_bars[b], (ring.used / Cfg::EPI_BUFS) & 1u, sh, limit));
+                        if (ok) unstage_row128(smem_u32(buf), lane, w);
                     } else if (lane_row) {
                         load_row_bf16<8>(static_cast<const uint16_t *>(p.z) + row * p.ldz + 2 * col0, w, zleft);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = 0u;
                     }
-                    act.backward<16>(v, w);
-                    act.backward<16>(v + 16, w + 16);
+                    __syncwarp();
+                    tmem_ld_wait_x32(v);
+                    if (j + Cfg::SPLIT >= BN / 32) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
+                    }
+                    if (!ok) break;
+                    if (!used) continue;
+                    act.backward<8>(v, w);
+                    act.backward<8>(v + 16, w + 16);
                     if (in_ring) {
                         stage_row128(smem_u32(buf), lane, w);
                         fence_proxy_async_smem();

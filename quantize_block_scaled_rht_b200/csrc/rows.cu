@@ -156,10 +156,10 @@ __global__ void __launch_bounds__(THREADS) gated_rows_kernel(const GatedRowsPara
 #pragma unroll
             for (int k = 0; k < KSPLIT; ++k) z[e] = __fadd_rn(z[e], red[k][2 * pr + e][m]);
         }
-        const uint32_t v[2] = {__float_as_uint(z[0]), __float_as_uint(z[1])};
-        float h;
+        const uint32_t v[4] = {__float_as_uint(z[0]), __float_as_uint(z[1]), 0u, 0u};
+        float2 h;
         p.act.forward<1>(v, &h);
-        p.h[m * p.ldh + n / 2] = (uint16_t)pack_bf16x2(h, 0.0f);
+        p.h[m * p.ldh + n / 2] = (uint16_t)pack_bf16x2(h.x, 0.0f);
         if (p.z) *reinterpret_cast<uint32_t *>(p.z + m * p.ldz + n) = pack_bf16x2(z[0], z[1]);
     }
 }
