@@ -229,10 +229,12 @@ constexpr int MODE_DENSE = 0, MODE_GROUPED_M = 1, MODE_GROUPED_K = 2;
 // Pair tile t -> coordinates.  Dense: M in steps of 256 (fastest), then N.
 // Grouped rows: group g owns cum[g+1] - cum[g] pair tiles.  Grouped K: group
 // g owns tiles_m x tiles_n tiles of its [M, N] output over K range
-// [cum[g], cum[g+1]) (cum holds the validated K offsets).
+// [cum[g], cum[g+1]) (cum holds the validated K offsets).  g_at: a group at or
+// before the tile's, from which the search goes on (a role's tiles only grow);
+// with 32 groups a search from the first one cost each role 700 cycles a tile.
 template <int BN, int MODE>
 __device__ __forceinline__ TileInfo get_tile(int t, uint32_t rank, const GemmParams &p, const int *cum,
-                                             int tiles_n) {
+                                             int tiles_n, int &g_at) {
     TileInfo ti;
     ti.k0 = 0;
     ti.kg = p.K;
@@ -260,8 +262,9 @@ __device__ __forceinline__ TileInfo get_tile(int t, uint32_t rank, const GemmPar
         ti.sfb_rt_base = 0;
         ti.c_row0 = ti.row0;
     } else {
-        int g = 0;
+        int g = g_at;
         while (g + 1 < p.num_groups && cum[g + 1] <= t) ++g;
+        g_at = g;
         const int local = t - cum[g];
         const int tiles_g = (cum[g + 1] - cum[g]) / tiles_n;
         const int tm = local % tiles_g, tn = local / tiles_g;
@@ -370,18 +373,18 @@ __device__ __forceinline__ bool ragged_box(int64_t col, int width, int64_t ncols
 // past their group's rows, and ragged ones, do not go through the ring.
 template <class Cfg, int MODE>
 struct ZRing {
-    int t, j;                // next box to look at: pair tile, 32-column step
+    int t, j, g_at;          // next box to look at: pair tile, 32-column step; its group
     uint32_t issued, used;
     TileInfo ti;
     static constexpr uint32_t AHEAD = Cfg::EPI_BUFS - 2;
 
-    __device__ __forceinline__ void start(int t0, int part) { t = t0; j = part; issued = used = 0; }
+    __device__ __forceinline__ void start(int t0, int part) { t = t0; j = part; g_at = 0; issued = used = 0; }
     // Issue loads until AHEAD boxes past the current one are in flight.
     __device__ __forceinline__ void fill(const CUtensorMap *map, uint8_t *bufs, uint64_t *bars, const GemmParams &p,
                                          const int *cum, int tiles_n, int ntiles, int npairs, uint32_t rank,
                                          int row_lo, int lane, int part) {
         while (issued < used + AHEAD + 1 && t < ntiles) {
-            if (j == part) ti = get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n);
+            if (j == part) ti = get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n, g_at);
             const bool boxes = row_lo < ti.rows_valid && (MODE == MODE_DENSE || row_lo + 32 <= ti.rows_valid);
             const int64_t col0 = ti.n0 + 32 * j;
             if (boxes && col0 < p.N && !ragged_box(2 * col0, 64, 2 * p.N, 2)) {
@@ -577,10 +580,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         const bool issuer = elect_one();
         {
             uint32_t armed = 0, armed_par = 0;   // even CTA: stages armed, parity of the last arm
-            int s = 0;
+            int s = 0, g_at = 0;
             uint32_t ph = 0;
             for (int t = pair; t < ntiles && !sh->abort; t += npairs) {
-                const TileInfo ti = get_tile<BN, MODE>(t, rank, p, cum, tiles_n);
+                const TileInfo ti = get_tile<BN, MODE>(t, rank, p, cum, tiles_n, g_at);
                 const int32_t sfa_rt = (int32_t)(ti.row0 / 128);
                 const int32_t sfb_rt = (int32_t)(ti.sfb_rt_base + ti.n0 / 128);
                 const int ktiles = ktiles_of(ti);
@@ -634,10 +637,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             bool issued = false;
             int s = 0;
             uint32_t ph = 0, kglobal = 0;
-            int acc = 0;
+            int acc = 0, g_at = 0;
             uint32_t acc_ph = 0;
             for (int t = pair; t < ntiles && !sh->abort; t += npairs) {
-                const TileInfo ti = get_tile<BN, MODE>(t, 0, p, cum, tiles_n);
+                const TileInfo ti = get_tile<BN, MODE>(t, 0, p, cum, tiles_n, g_at);
                 const int64_t rt0 = ti.n0 / 128;
                 const uint32_t b_shift = (uint32_t)((ti.n0 - rt0 * 128) / 32);
                 if (!wait_phase(&sh->tmem_empty[acc], acc_ph ^ 1u, sh, limit)) break;
@@ -692,8 +695,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         uint8_t *ring_bufs = epi_base + ew * Cfg::EPI_BUFS * EPI_BUF;
         uint64_t *ring_bars = zbar + (OUT == OUT_GATED_BWD ? ew * Cfg::EPI_BUFS : 0);
         ring.start(pair, part);
+        int g_at = 0;
         for (int t = pair; t < ntiles; t += npairs) {
-            const TileInfo ti = get_tile<BN, MODE>(t, rank, p, cum, tiles_n);
+            const TileInfo ti = get_tile<BN, MODE>(t, rank, p, cum, tiles_n, g_at);
             const int row_lo = 32 * q;
             // int8: this lane's token scale, and the channel scale of column
             // 32 j + lane of the tile, one 32-column step ahead
