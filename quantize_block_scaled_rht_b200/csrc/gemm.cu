@@ -531,22 +531,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     pdl_wait();
     pdl_trigger();
     if constexpr (GROUPED) {
-        if (threadIdx.x == 32 * 2) {
+        if (warp == 2) {
+            // 32 groups at a time: their loads together, their tile counts summed
+            // by a warp scan
             int acc = 0;
-            for (int g = 0; g < p.num_groups; ++g) {
-                cum[g] = acc;
-                const int64_t off = p.group_offsets[g], nxt = p.group_offsets[g + 1];
-                const int64_t size = p.group_sizes[g];
-                int tm = 0;
-                if ((off % BM) != 0 || size < 0 || off + size > nxt || nxt > p.M) {
-                    if (rank == 0) record_error(MXFP4_ERR_INVALID_ARG);
-                } else {
-                    tm = (int)((size + 255) / 256);
+            for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
+                const int g = g0 + lane;
+                int tiles = 0;
+                if (g < p.num_groups) {
+                    const int64_t off = p.group_offsets[g], nxt = p.group_offsets[g + 1];
+                    const int64_t size = p.group_sizes[g];
+                    if (off < 0 || (off % BM) != 0 || size < 0 || off + size > nxt || nxt > p.M) {
+                        if (rank == 0) record_error(MXFP4_ERR_INVALID_ARG);
+                    } else {
+                        tiles = (int)((size + 255) / 256) * tiles_n;
+                    }
                 }
-                acc += tm * tiles_n;
+                int sum = tiles;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int below = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                    if (lane >= d) sum += below;
+                }
+                if (g < p.num_groups) cum[g] = acc + sum - tiles;
+                acc += __shfl_sync(0xFFFFFFFFu, sum, 31);
             }
-            cum[p.num_groups] = acc;
-            sh->ntiles = acc;
+            if (lane == 0) {
+                cum[p.num_groups] = acc;
+                sh->ntiles = acc;
+            }
         }
     } else if constexpr (MODE == MODE_GROUPED_K) {
         if (threadIdx.x == 32 * 2) {

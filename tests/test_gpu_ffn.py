@@ -158,13 +158,18 @@ def test_grouped_gated_gemm(sizes, I, K, keep):
         assert torch.all(zo[~torch.from_numpy(written)] == 9)
 
 
-def test_grouped_gated_bad_offset_is_reported():
+@pytest.mark.parametrize("offsets,sizes,kept", [([0, 100, 256], [10, 20], 100), ([-128, 0, 256], [10, 20], 20),
+                                                 ([0, 128, 512], [10, 300], 10), ([128, 0, 256], [10, 20], 20),
+                                                 ([0, 128, 256], [-5, 129], 0)])
+def test_grouped_gated_bad_groups_are_reported_and_skipped(offsets, sizes, kept):
+    """Groups off a 128-row boundary, before the first row, past the end, backwards,
+    of a negative or too large size: reported, and nothing of them is written."""
     c = grouped_operands([10, 20], 64, 64, 3, 1.0, 0.2)
-    bad = torch.tensor([0, 100, 256], dtype=torch.int32, device="cuda")
-    out = torch.zeros((c["rows"], 32), dtype=torch.bfloat16, device="cuda")
-    mx.mxfp4_grouped_gated_gemm(c["a"][2], c["a"][3], bad, c["d_sizes"], c["b"], c["sb"], 64, out=out)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.full((c["rows"], 32), 9.0, dtype=torch.bfloat16, device="cuda")
+    mx.mxfp4_grouped_gated_gemm(c["a"][2], c["a"][3], i32(offsets), i32(sizes), c["b"], c["sb"], 64, out=out)
     assert mx.mxfp4_get_error() == mx.MXFP4_ERR_INVALID_ARG
-    assert torch.all(out[100:] == 0)
+    assert torch.all(out[kept:] == 9)
     no_error()
 
 
