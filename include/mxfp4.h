@@ -451,7 +451,7 @@ MXFP4_API int mxfp4_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_
  * once; its sums differ from the tile kernel's in their last bits.
  *
  * Requirements: as mxfp4_gemm / mxfp4_grouped_gemm; N even; h and z 16-byte
- * aligned, ldh % 8 == 0, ldz % 8 == 0, not overlapping; alpha and beta finite,
+ * aligned, ldh % 8 == 0, ldz % 8 == 0, sharing no element; alpha and beta finite,
  * limit > 0.
  */
 MXFP4_API int mxfp4_gated_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales,
@@ -474,7 +474,8 @@ MXFP4_API int mxfp4_grouped_gated_gemm(const uint8_t *a_codes, int64_t lda, cons
  *     dz[2j]     = dh[j] (u + beta) s (1 + alpha g (1 - s))   where z[2j] <= limit, else 0
  *     dz[2j + 1] = dh[j] g s                                  where |z[2j + 1]| <= limit, else 0
  * dz bf16 [M or a_rows, 2N] (lddz), rounded once; a NaN in z gives NaN.  dz
- * may be z itself (same pointer and row stride); any other overlap is refused.
+ * may be z itself (same pointer and row stride), or other columns of its buffer;
+ * any other overlap is refused.
  * The gradients of X and of the gate_up weight follow from dz by
  * mxfp4_quantize_dual and the products of mxfp4_gemm and
  * mxfp4_grouped_gemm_wgrad.  Requirements as for the forward form (N need not
@@ -543,8 +544,8 @@ MXFP4_API int mxfp4_int8_grouped_gemm(const int8_t *a_codes, int64_t lda, const 
  * dtype: MXFP4_OUT_BF16 or MXFP4_OUT_F32, of x, residual (NULL = none) and y.
  * Any sizes, row strides (elements) and element alignment; 16-byte aligned
  * pointers with rows of whole 16-byte pieces (or contiguous tensors) run
- * fastest.  y may be x or residual itself (same pointer and row stride); any
- * other overlap is refused.
+ * fastest.  y may be x or residual itself (same pointer and row stride), or
+ * other columns of their buffer; any other overlap is refused.
  * Requirements: rows, cols > 0; 0 <= p <= 1; elem_offset % 4 == 0.
  */
 MXFP4_API int mxfp4_dropout(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual,

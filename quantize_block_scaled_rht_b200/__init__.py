@@ -826,6 +826,8 @@ def mxfp4_dropout(x: torch.Tensor, p: float, seed: int, elem_offset: int = 0, re
     kind = x.dtype
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be within [0, 1], got {p}")
+    if elem_offset < 0:
+        raise ValueError(f"elem_offset must not be negative, got {elem_offset}")
     pr, ldr = None, 0
     if residual is not None:
         pr, ldr = residual.data_ptr(), _rows_of(residual, "residual", kind, rows, cols)

@@ -432,6 +432,17 @@ static bool valid_act(float alpha, float limit, float beta) {
     return std::isfinite(alpha) && limit > 0.0f && std::isfinite(beta);   // limit may be infinite
 }
 
+// Whether two row-major arrays of `rows` rows (row strides and widths in bytes)
+// share no byte: apart in memory, or different columns of one buffer.
+static bool disjoint(const void *p, int64_t ld_p, int64_t w_p, const void *q, int64_t ld_q, int64_t w_q, int64_t rows) {
+    const char *p0 = static_cast<const char *>(p), *q0 = static_cast<const char *>(q);
+    const char *p1 = p0 + (rows - 1) * ld_p + w_p, *q1 = q0 + (rows - 1) * ld_q + w_q;
+    if (p1 <= q0 || q1 <= p0) return true;
+    if (ld_p != ld_q) return false;
+    const int64_t d = ((q0 - p0) % ld_p + ld_p) % ld_p;      // column of q in p's rows
+    return w_p <= d && d + w_q <= ld_p;
+}
+
 // Row-major bf16 [rows, cols]: 16-byte rows.
 static int check_bf16(const void *p, int64_t ld, int64_t cols) {
     if (!p || ld < cols) return MXFP4_ERR_INVALID_ARG;
@@ -456,12 +467,9 @@ static int gated_impl(const mxfp4::GatedArgs &a, void *stream) {
         if (rc != MXFP4_OK) return rc;
     }
     // z and the output: apart, or (backward) the same buffer with the same rows
-    if (a.z && !(a.backward && a.z == a.out && a.ldz == a.ld_out)) {
-        const char *z0 = static_cast<const char *>(a.z), *o0 = static_cast<const char *>(a.out);
-        const char *z1 = z0 + 2 * ((a.M - 1) * a.ldz + zcols);
-        const char *o1 = o0 + 2 * ((a.M - 1) * a.ld_out + (a.backward ? 2 * a.N : a.N / 2));
-        if (z0 < o1 && o0 < z1) return MXFP4_ERR_INVALID_ARG;
-    }
+    if (a.z && !(a.backward && a.z == a.out && a.ldz == a.ld_out) &&
+        !disjoint(a.z, 2 * a.ldz, 2 * zcols, a.out, 2 * a.ld_out, a.backward ? 4 * a.N : a.N, a.M))
+        return MXFP4_ERR_INVALID_ARG;
     if (a.M > (int64_t)1 << 31 || a.N > (int64_t)1 << 30) return MXFP4_ERR_UNSUPPORTED;
     return mxfp4::launch_gated(a, static_cast<cudaStream_t>(stream));
 }
@@ -574,10 +582,10 @@ int mxfp4_dropout(const void *x, int64_t ld_x, const void *residual, int64_t ld_
         reinterpret_cast<uintptr_t>(residual) % size)
         return MXFP4_ERR_ALIGNMENT;
     // in place element for element (y over x or over the residual), or apart
-    const char *y0 = static_cast<const char *>(y), *y1 = y0 + size * ((rows - 1) * ld_y + cols);
+    const int64_t sz = (int64_t)size, w = sz * cols;
     auto bad = [&](const void *q, int64_t ld) {
-        const char *q0 = static_cast<const char *>(q), *q1 = q0 + size * ((rows - 1) * ld + cols);
-        return q && !(q0 == y0 && (rows == 1 || ld == ld_y)) && q0 < y1 && y0 < q1;
+        return q && !(q == y && (rows == 1 || ld == ld_y)) &&
+               !disjoint(q, rows == 1 ? w : sz * ld, w, y, rows == 1 ? w : sz * ld_y, w, rows);
     };
     if (bad(x, ld_x) || bad(residual, ld_residual)) return MXFP4_ERR_INVALID_ARG;
     const cudaError_t e = mxfp4::launch_dropout(x, ld_x, residual, ld_residual, rows, cols, dtype, p, seed, elem_offset,

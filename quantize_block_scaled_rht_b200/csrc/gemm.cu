@@ -725,7 +725,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             }
             if constexpr (OUT == OUT_GATED_BWD)
                 ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
-            if (!wait_phase(&sh->tmem_full[acc], acc_ph, sh, limit)) break;
+            // one answer for the warp: what follows needs it whole
+            if (!__all_sync(0xFFFFFFFFu, wait_phase(&sh->tmem_full[acc], acc_ph, sh, limit))) break;
             tc_fence_after();
             const bool full_box = MODE == MODE_DENSE || (row_lo + 32 <= ti.rows_valid);
             const bool any_row = row_lo < ti.rows_valid;

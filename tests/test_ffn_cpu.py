@@ -90,6 +90,23 @@ def test_gated_backward_refusals(kw, want):
     assert _bwd(**kw) == want
 
 
+def test_columns_of_one_buffer_are_not_an_overlap():
+    """Refused only where elements are shared: the calls below pass the overlap check
+    and fail at a later one (a row count, an offset), so nothing is launched."""
+    L = mx.lib()
+    at = lambda off: ctypes.c_void_p(0x10000 + off)  # noqa: E731
+    # bf16 rows of 64 elements: x in columns 0-31, y in 32-63 (apart) or 16-47 (shared)
+    drop = lambda y, ld_y: L.mxfp4_dropout(at(0), 64, None, 0, 1 << 40, 32, mx.OUT_BF16, 0.5, 1, 0, at(y), ld_y, None)  # noqa: E731
+    assert drop(32, 64) == mx.MXFP4_ERR_INVALID_ARG and drop(2 * 64 * 3 + 32, 64) == mx.MXFP4_ERR_INVALID_ARG
+    assert drop(64, 72) == mx.MXFP4_ERR_INVALID_ARG
+    big = 1 << 32                      # rows: unsupported, checked after the overlap
+    bwd = lambda dz, ld: L.mxfp4_gated_gemm_backward(  # noqa: E731
+        FAKE, 32, FAKE, FAKE, 32, FAKE, big, 16, 64, 1.0, INF, 0.0, at(0), 64, at(dz), ld, None)
+    assert bwd(64, 64) == mx.MXFP4_ERR_UNSUPPORTED and bwd(0, 64) == mx.MXFP4_ERR_UNSUPPORTED
+    assert bwd(32, 64) == mx.MXFP4_ERR_INVALID_ARG and bwd(64, 72) == mx.MXFP4_ERR_INVALID_ARG
+    assert bwd(128 * 5 + 64, 64) == mx.MXFP4_ERR_UNSUPPORTED and bwd(128 * 5 + 96, 64) == mx.MXFP4_ERR_INVALID_ARG
+
+
 def test_grouped_gated_refusals():
     L = mx.lib()
     f = lambda off=FAKE, sizes=FAKE, G=2, N=128: L.mxfp4_grouped_gated_gemm(  # noqa: E731
@@ -188,6 +205,8 @@ def test_bindings_refuse_before_the_abi():
         mx.mxfp4_dropout(f(4, 4).half(), 0.1, 1)
     with pytest.raises(ValueError, match="residual must be"):
         mx.mxfp4_dropout(f(4, 4), 0.1, 1, residual=bf(4, 4))
+    with pytest.raises(ValueError, match="elem_offset"):
+        mx.mxfp4_dropout(f(4, 4), 0.1, 1, elem_offset=-4)
     for p in (-0.5, 1.5, float("nan")):
         with pytest.raises(ValueError, match="p must be"):
             mx.mxfp4_dropout(f(4, 4), p, 1)

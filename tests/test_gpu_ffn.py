@@ -59,6 +59,7 @@ def no_error():
 # ------------------------------------------------------------------ gated product
 FWD = [(1, 8, 64), (2, 96, 128), (3, 1000, 64), (7, 40, 2880), (8, 96, 4160), (9, 96, 128), (37, 48, 192), (128, 96, 512), (130, 104, 320),
        (300, 200, 2880), (257, 500, 576), (513, 64, 64),
+       (4, 16, 12032), (3, 16, 4096),
        (1100, 2500, 128), (2600, 700, 320)]
 
 
@@ -597,6 +598,84 @@ def test_graph_capture_replay_and_side_streams():
             for c, e in zip(captured, step()):
                 assert torch.equal(c, e)
         no_error()
+
+
+def test_outputs_in_other_columns_of_the_inputs_buffer():
+    M, I, K = 150, 40, 128
+    _, _, da, dsa = operand(M, K, 1, 1e-2)
+    _, _, db, dsb = operand(I, K, 2, 0.1)
+    buf = torch.zeros((M, 4 * I), dtype=torch.bfloat16, device="cuda")
+    buf[:, :2 * I] = dev_bf16(z_values(M, I, 3))
+    want = mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, buf[:, :2 * I].clone(), K)
+    mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, buf[:, :2 * I], K, out=buf[:, 2 * I:])
+    assert torch.equal(buf[:, 2 * I:], want)
+    x = torch.randn((30, 64), generator=torch.Generator().manual_seed(1)).cuda()
+    want = mx.mxfp4_dropout(x[:, :32].clone(), 0.3, 4)
+    mx.mxfp4_dropout(x[:, :32], 0.3, 4, out=x[:, 32:])
+    assert torch.equal(x[:, 32:], want)
+
+
+def test_calls_at_once_on_two_streams():
+    """The operators keep no state between calls: two streams at once give what one gives."""
+    M, I, K = 520, 384, 512
+    ops = [(operand(M, K, 10 + i, 1.0)[2:], operand(2 * I, K, 20 + i, 0.1)[2:], operand(I, K, 30 + i, 0.1)[2:]) for i in range(2)]
+    w8 = mx.mxfp4_int8_quantize(dev_bf16(synth.normal_bf16((200, I), 5, 0.1)))
+
+    def step(i, stream=None):
+        (a, sa), (b, sb), (t, st) = ops[i]
+        h, z = mx.mxfp4_gated_gemm(a, sa, b, sb, K, **ffn.CLAMPED, save_z=True, stream=stream)
+        dz = mx.mxfp4_gated_gemm_backward(a, sa, t, st, z, K, **ffn.CLAMPED, stream=stream)
+        q = mx.mxfp4_int8_quantize(h, stream=stream)
+        y = mx.mxfp4_int8_gemm(q.codes, q.scales, w8.codes, w8.scales, stream=stream)
+        return h, z, dz, q.codes, q.scales, mx.mxfp4_dropout(y, 0.2, i, stream=stream)
+
+    want = [[t.clone() for t in step(i)] for i in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[step(i, streams[i]) for i in range(2)] for _ in range(20)]
+    torch.cuda.synchronize()
+    no_error()
+    for pair in got:
+        for w, g in zip(want, pair):
+            assert all(torch.equal(x, y) for x, y in zip(w, g))
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import torch
+import quantize_block_scaled_rht_b200 as mx
+g = torch.Generator(device="cuda").manual_seed(1)
+u8 = lambda *s: torch.randint(0, 256, s, dtype=torch.uint8, device="cuda", generator=g)
+M, I, K = int(sys.argv[2]), 96, 256
+a, b, t = u8(M, K // 2), u8(2 * I, K // 2), u8(I, K // 2)
+sc = lambda n: torch.full((mx.mma_scales_bytes(n, K),), 124, dtype=torch.uint8, device="cuda")
+sa, sb, st = sc(M), sc(2 * I), sc(I)
+w, ws = torch.randint(-127, 128, (64, I), dtype=torch.int8, device="cuda", generator=g), torch.rand(64, device="cuda", generator=g)
+def step():
+    h, z = mx.mxfp4_gated_gemm(a, sa, b, sb, K, save_z=True)
+    dz = mx.mxfp4_gated_gemm_backward(a, sa, t, st, z, K)
+    q = mx.mxfp4_int8_quantize(h)
+    y = mx.mxfp4_int8_gemm(q.codes, q.scales, w, ws)
+    return h, z, dz, q.codes, y, mx.mxfp4_dropout(y, 0.2, 3)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, step())) and mx.mxfp4_get_error() == 0
+print("ok")
+"""
+
+
+@pytest.mark.parametrize("M", [2, 300])
+def test_first_call_of_a_process_inside_a_capture(M):
+    import subprocess
+    import sys
+    from conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL, ROOT, str(M)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
 
 
 def test_repeated_calls_give_the_same_bits():
