@@ -163,6 +163,7 @@ struct GemmParams {
     int64_t ldz;
     float act_alpha, act_limit, act_beta;
     int num_groups;
+    uint32_t stage_tx;         // bytes of both CTAs' loads of one stage
     uint64_t wait_limit_ns;
 };
 
@@ -611,11 +612,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                         armed_par = (armed_par & ~(1u << s)) | (ph << s);
                     }
                     if (issuer) {
-                        if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], Cfg::STAGE_TX);
+                        if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], p.stage_tx);
 #pragma unroll
                         for (int c = 0; c < KCH; ++c) {
                             const int32_t kx = (int32_t)(ti.k0 / Cfg::KPB) + (kt * KCH + c) * CHUNK;
-                            tma_load_2d_pair(st + c * Cfg::A_CHUNK, &tma_a, kx, (int32_t)ti.row0, full_leader);
+                            // (dense, one row tile: the odd CTA has no rows of A)
+                            if (MODE != MODE_DENSE || rank == 0 || p.M > BM)
+                                tma_load_2d_pair(st + c * Cfg::A_CHUNK, &tma_a, kx, (int32_t)ti.row0, full_leader);
                             tma_load_2d_pair(st + A_BYTES + c * Cfg::B_CHUNK, &tma_b, kx,
                                              (int32_t)(ti.b_row + rank * (BN / 2)), full_leader);
                         }
@@ -1155,11 +1158,16 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     const int64_t c_rows = MODE == MODE_GROUPED_K ? (int64_t)g.G * g.M : g.M;
     const int64_t katoms = (g.K + Cfg::KATOM - 1) / Cfg::KATOM;
     const int64_t a_tiles = (g.M + 127) / 128, b_tiles = (g.N + 127) / 128;
+    // Few rows: filling the box's rows past M is slower than loading rows, so the
+    // box is as high as it has to be and the odd CTA loads none (what stands in
+    // shared memory there only reaches rows that are not stored).  16 rows of
+    // 178560 x 2880: 88 -> 60 us.
+    const uint32_t a_box = MODE == MODE_DENSE && g.M <= 64 ? (g.M <= 32 ? 32 : 64) : BM;
     CUtensorMap ta, tb, tc, tz, tsa, tsb;
     constexpr CUtensorMapDataType BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     constexpr CUtensorMapSwizzle SW128 = CU_TENSOR_MAP_SWIZZLE_128B;
     const uint64_t kbytes = (uint64_t)(g.K / Cfg::KPB), N = (uint64_t)g.N, ldc = (uint64_t)g.ldc;
-    bool ok = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a_codes, kbytes, (uint64_t)g.M, (uint64_t)g.lda, CHUNK, BM,
+    bool ok = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a_codes, kbytes, (uint64_t)g.M, (uint64_t)g.lda, CHUNK, a_box,
                        SW128) &&
               make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b_codes, kbytes, (uint64_t)G * N, (uint64_t)g.ldb, CHUNK,
                        BN / 2, SW128);
@@ -1199,6 +1207,8 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     p.z = g.z; p.ldz = g.ldz;
     p.act_alpha = g.alpha; p.act_limit = g.limit; p.act_beta = g.beta;
     p.wait_limit_ns = g_wait_limit_ns;
+    p.stage_tx = Cfg::STAGE_TX - (uint32_t)(Cfg::KCH * (BM - a_box) * CHUNK) -
+                 (MODE == MODE_DENSE && g.M <= BM ? (uint32_t)Cfg::A_BYTES : 0u);
     const int pairs_max = sm_count() / 2;
     int pairs = pairs_max;
     if (MODE != MODE_GROUPED_M) {
