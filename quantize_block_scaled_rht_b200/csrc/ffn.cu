@@ -28,9 +28,12 @@ __device__ __forceinline__ void st_v2(void *p, uint32_t a, uint32_t b) {
 // steps of 2^-24 of 127 / a, so |x i| stays below 127.5).  The floor keeps 1 / a
 // finite; a NaN or Inf anywhere in the row gives the scale NaN and codes 0.
 //
-// Bound by HBM (2 B read, 1 B written per element).  T threads hold one row in
-// registers (V 16-byte vectors each), so it is read once; a row that does not
-// fit takes V = 0, which reads it twice (the second time mostly from L2).
+// Bound by HBM (2 B read, 1 B written per element; 16384 x 11520: 81 us, 7.0 TB/s
+// with part of the writes still in L2).  T threads hold one row in registers (V
+// 16-byte vectors each), so it is read once; a row that does not fit takes V = 0,
+// which reads it twice (the second time mostly from L2).  T grows with the row so
+// that a thread has no more than eight loads in flight and short rows still fill
+// the SMs.
 // ---------------------------------------------------------------------------
 
 // Largest magnitude of 8 bf16 as two 16-bit halves (NaN where there is one).
@@ -165,6 +168,7 @@ struct DropParams {
     uint64_t block0;               // elem_offset / 4
     uint32_t k0, k1, last;         // dropped: words up to `last` = round(p 2^32) - 1
     float scale;
+    uint32_t key0[10], key1[10];   // the rounds' keys, operands straight from the constant bank
 };
 
 // ALL: round(p 2^32) is 0, every element is kept and no word is drawn.
@@ -192,8 +196,17 @@ struct DropCounter {
     }
     __device__ __forceinline__ U4 words(uint32_t lo, const DropParams &p) const {
         const uint64_t a = (uint64_t)0xD2511F53u * lo;
-        const uint64_t b = (uint64_t)0xCD9E8D57u * ((uint32_t)(a >> 32) ^ (DROPOUT_TAG ^ p.k1));
-        return philox_rounds<2>((uint32_t)(b >> 32) ^ (p.k0 + 0x9E3779B9u), (uint32_t)b, (uint32_t)a ^ x, c3, p.k0, p.k1);
+        const uint64_t b = (uint64_t)0xCD9E8D57u * ((uint32_t)(a >> 32) ^ (DROPOUT_TAG ^ p.key1[0]));
+        uint32_t c0 = (uint32_t)(b >> 32) ^ p.key0[1], c1 = (uint32_t)b, c2 = (uint32_t)a ^ x, w3 = c3;
+#pragma unroll
+        for (int r = 2; r < 10; ++r) {
+            const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
+            c0 = (uint32_t)(p1 >> 32) ^ c1 ^ p.key0[r];
+            c2 = (uint32_t)(p0 >> 32) ^ w3 ^ p.key1[r];
+            c1 = (uint32_t)p1;
+            w3 = (uint32_t)p0;
+        }
+        return U4{c0, c1, c2, w3};
     }
 };
 
@@ -203,10 +216,13 @@ struct DropCounter {
 // high counter half (any tensor below 2^34 elements, but for an offset that
 // happens to cross a multiple of that).
 //
-// Bound by HBM with the residual or in FP32; plain bf16 by its integer
-// instructions, which all issue at one per two cycles: of about 116 per 8
-// elements Philox is 78.  65536 x 2880: 154 us (0.75 of HBM); with addresses
-// from row and column and every word from scratch 180; without drawing 118.
+// Bound by HBM with the residual (65536 x 2880: 174 us, the measured copy
+// bandwidth) or in FP32; plain bf16 by the issue of its instructions, 130 per 8
+// elements, of which Philox is about 80 (61% of the issue slots, the integer
+// multiply pipe 74% busy): 150 us, 0.77 of HBM.  With addresses from row and
+// column and every word from scratch 180, with the rounds' keys added up in the
+// kernel 154, with the shift of the low bf16 moved off the multiply pipe 155;
+// without drawing 118.
 template <bool BF16, bool RES, bool ALL, bool FLAT>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropParams p) {
     pdl_wait();
@@ -335,8 +351,12 @@ cudaError_t launch_dropout(const void *x, int64_t ld_x, const void *residual, in
                            int64_t cols, int dtype, double prob, uint64_t seed, uint64_t elem_offset, void *y,
                            int64_t ld_y, cudaStream_t s) {
     const double t = std::nearbyint(prob * 4294967296.0);   // 0 .. 2^32
-    const DropParams p{x, residual, y, rows, cols, ld_x, ld_residual, ld_y, elem_offset / 4, (uint32_t)seed,
-                       (uint32_t)(seed >> 32), t > 0.0 ? (uint32_t)(t - 1.0) : 0u, prob < 1.0 ? (float)(1.0 / (1.0 - prob)) : 0.0f};
+    DropParams p{x, residual, y, rows, cols, ld_x, ld_residual, ld_y, elem_offset / 4, (uint32_t)seed,
+                       (uint32_t)(seed >> 32), t > 0.0 ? (uint32_t)(t - 1.0) : 0u, prob < 1.0 ? (float)(1.0 / (1.0 - prob)) : 0.0f, {}, {}};
+    for (uint32_t r = 0; r < 10; ++r) {
+        p.key0[r] = p.k0 + r * 0x9E3779B9u;
+        p.key1[r] = p.k1 + r * 0xBB67AE85u;
+    }
     const bool bf16 = dtype == MXFP4_OUT_BF16, res = residual != nullptr;
     if (t == 0.0)
         return bf16 ? (res ? run_dropout<true, true, true>(p, s) : run_dropout<true, false, true>(p, s))

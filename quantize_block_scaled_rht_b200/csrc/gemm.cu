@@ -1,4 +1,5 @@
-// gemm.cu -- MXFP4 block-scaled GEMM (dense and grouped) for sm_100a.
+// gemm.cu -- MXFP4 block-scaled GEMM (dense and grouped) for sm_100a, with the
+// gated epilogues of the expert feed-forward block and the int8 product.
 //
 // "MXFP4" (aiwiki.ai), "Conversion rules": the block dot product
 // C = X(A) X(B) sum_i Pi(A) Pi(B), block products summed, FP32 result; the
@@ -23,7 +24,8 @@
 //   warps 2..5  epilogue: TMEM -> registers -> swizzled smem -> TMA store of
 //               this CTA's 128 rows (FP32, or bf16 rounded to nearest even),
 //               overlapping the next tile's MMAs, then an arrive on the even
-//               CTA's accumulator-empty barrier.
+//               CTA's accumulator-empty barrier (warps 2..9 with the gated
+//               activation or its derivative in the epilogue).
 // Every barrier wait is bounded by the GPU global timer; a wait that runs out
 // records MXFP4_ERR_TIMEOUT, raises the CTA's abort flag, and each role drains
 // what it has in flight before both CTAs meet at the final cluster barrier.
