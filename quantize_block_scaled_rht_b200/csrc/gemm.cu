@@ -123,16 +123,17 @@ using NvCfg = TileCfg<192, 5, 1, KIND_NV>;
 // The gated epilogues take eight warps.  Forward: one staging buffer each, which
 // keeps the 3 x 512 ring (4096 x 5760 x 2880, h alone: 35.1 us, the bf16
 // product's time; 4 warps and two buffers 48.8, 8 warps and two buffers on a
-// ring of 5 x 256 40.2).  Backward: three buffers carry z in and dz out, paid for
-// with a ring of 4 x 256 (4096 x 2880 x 2880: 38.3 us; 4 warps, four buffers and
-// a ring of 5 x 256 43.3; packed FP32 and z read beside the accumulators 36.8).
+// ring of 5 x 256 40.2).  Backward: two buffers carry z in and dz out, beside a
+// ring of 5 x 256 (4096 x 2880 x 2880 37.0 us, K = 5760 50.8; three buffers and a
+// ring of 4 x 256 37.0 and 54.2, four of 3 x 256 41.7 and 61.6, 4 warps 43.3, 12
+// warps 41.2).
 using GatedCfg = TileCfg<192, 3, 2, KIND_MX, 1, 8>;
-using BwdCfg = TileCfg<192, 4, 1, KIND_MX, 3, 8>;
+using BwdCfg = TileCfg<192, 5, 1, KIND_MX, 2, 8>;
 // Dense calls take 128-column tiles where those finish in clearly fewer rounds
 // of tiles (launch_dense): 256 x 5760 x 2880 8.0 against 9.1 us, 768 rows 11.5
 // against 13.0; backward, 768 x 2880 x 2880, 12.4 against 14.1.
 using GatedNarrowCfg = TileCfg<128, 3, 2, KIND_MX, 2, 8>;
-using BwdNarrowCfg = TileCfg<128, 4, 1, KIND_MX, 3, 8>;
+using BwdNarrowCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8>;
 // int8: without scale factors in tensor memory two 256-column accumulators fit,
 // and a 256 x 256 tile reads 1/8 fewer operand bytes per product than 256 x 192
 // (4096 x 2880 x 2880: 28.6 us, 256 x 192 33.8, and 31.7 with the ring as 3 x 256
@@ -369,31 +370,29 @@ __device__ __forceinline__ bool ragged_box(int64_t col, int width, int64_t ncols
 }
 
 // Backward epilogue, per warp: z boxes (32 rows x 64 columns, 4 KB) stream into
-// a ring of staging buffers by TMA, EPI_BUFS - 2 boxes ahead of the one
-// computed; each box is replaced in place by dz and stored.  Buffer n % EPI_BUFS
-// takes load n once the store of load n - EPI_BUFS has read it: of the stores
-// committed so far all but the newest must have been read.  Boxes that reach
+// two staging buffers by TMA, one box ahead of the one computed; each box is
+// replaced in place by dz and stored.  Load n goes into buffer n % 2 once the
+// store of box n - 2, the newest one committed, has read it.  Boxes that reach
 // past their group's rows, and ragged ones, do not go through the ring.
 template <class Cfg, int MODE>
 struct ZRing {
     int t, j, g_at;          // next box to look at: pair tile, 32-column step; its group
     uint32_t issued, used;
     TileInfo ti;
-    static constexpr uint32_t AHEAD = Cfg::EPI_BUFS - 2;
 
     __device__ __forceinline__ void start(int t0, int part) { t = t0; j = part; g_at = 0; issued = used = 0; }
-    // Issue loads until AHEAD boxes past the current one are in flight.
+    // Issue loads up to the box after the current one.
     __device__ __forceinline__ void fill(const CUtensorMap *map, uint8_t *bufs, uint64_t *bars, const GemmParams &p,
                                          const int *cum, int tiles_n, int ntiles, int npairs, uint32_t rank,
                                          int row_lo, int lane, int part) {
-        while (issued < used + AHEAD + 1 && t < ntiles) {
+        while (issued < used + 2 && t < ntiles) {
             if (j == part) ti = get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n, g_at);
             const bool boxes = row_lo < ti.rows_valid && (MODE == MODE_DENSE || row_lo + 32 <= ti.rows_valid);
             const int64_t col0 = ti.n0 + 32 * j;
             if (boxes && col0 < p.N && !ragged_box(2 * col0, 64, 2 * p.N, 2)) {
                 if (lane == 0) {
-                    const uint32_t b = issued % Cfg::EPI_BUFS;
-                    if (issued >= Cfg::EPI_BUFS) bulk_wait_group_read<1>();
+                    const uint32_t b = issued & 1u;
+                    if (issued >= 2) bulk_wait_group_read<0>();
                     mbar_arrive_expect_tx(&bars[b], EPI_BUF);
                     tma_load_2d(bufs + b * EPI_BUF, map, (int32_t)(2 * col0), (int32_t)(ti.c_row0 + row_lo), &bars[b]);
                 }
@@ -837,6 +836,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 }
             } else if constexpr (OUT == OUT_GATED_BWD) {
                 // 32 columns of dh per step with the 64 columns of z they belong to
+                static_assert(Cfg::EPI_BUFS == 2, "the ring has two buffers a warp");
                 const GatedAct act{p.act_alpha, p.act_limit, p.act_beta};
                 const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16) + (acc ? Cfg::ACC1_COL : 0u);
                 bool ok = true;
@@ -849,12 +849,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     const int64_t row = ti.c_row0 + row_lo + lane, zleft = 2 * (p.N - col0);
                     const bool lane_row = used && row_lo + lane < ti.rows_valid;
                     const bool in_ring = used && full_box && !ragged_box(2 * col0, 64, 2 * p.N, 2);
-                    const uint32_t b = ring.used % Cfg::EPI_BUFS;
+                    const uint32_t b = ring.used & 1u;
                     uint8_t *buf = ring_bufs + b * EPI_BUF;
                     if (in_ring) {
                         ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
                         // one answer for the warp: the tensor memory instructions need it whole
-                        ok = __all_sync(0xFFFFFFFFu, wait_phase(&ring_bars[b], (ring.used / Cfg::EPI_BUFS) & 1u, sh, limit));
+                        ok = __all_sync(0xFFFFFFFFu, wait_phase(&ring_bars[b], (ring.used >> 1) & 1u, sh, limit));
                         if (ok) unstage_row128(smem_u32(buf), lane, w);
                     } else if (lane_row) {
                         load_row_bf16<8>(static_cast<const uint16_t *>(p.z) + row * p.ldz + 2 * col0, w, zleft);
@@ -1020,8 +1020,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             // after an abort: loads in flight land before the shared memory goes away
             bool landed = true;
             for (; ring.used < ring.issued; ++ring.used)
-                landed &= wait_phase(&ring_bars[ring.used % Cfg::EPI_BUFS], (ring.used / Cfg::EPI_BUFS) & 1u, sh, limit,
-                                     true);
+                landed &= wait_phase(&ring_bars[ring.used & 1u], (ring.used >> 1) & 1u, sh, limit, true);
             if (!landed && lane == 0) mark_drain_failed(sh, rank);
         }
         if (lane == 0) bulk_wait_group_all();
