@@ -551,15 +551,18 @@ def mxfp4_scales_to_mma(scales: torch.Tensor, rows: int, k: int, two_d: bool = F
 
 # Host time counts where one token's kernels take a few microseconds, so the
 # common path (tensors on the current device, its current stream) does nothing
-# twice.
+# twice and looks nothing up twice.
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_U8, _I8, _BF16, _F32 = torch.uint8, torch.int8, torch.bfloat16, torch.float32
+
 
 def _run(fn, what: str, idx: int, stream, *args) -> None:
     """fn(*args, stream) on device idx; stream None = its current stream."""
-    if torch._C._cuda_getDevice() == idx:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else _stream(stream))
+    if _current_device() == idx:
+        rc = fn(*args, _raw_stream(idx) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(idx):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else _stream(stream))
+            rc = fn(*args, _raw_stream(idx) if stream is None else _stream(stream))
     if rc:
         raise MXFP4Error(rc, what)
 
@@ -590,17 +593,19 @@ def _empty(shape: tuple, strides: tuple, dtype: torch.dtype, idx: int, stream) -
 def _empty_rows(rows: int, cols: int, dtype: torch.dtype, idx: int, stream):
     """(tensor, its row stride): rows start on 16-byte boundaries, as the kernels
     store them, so the stride is above cols where cols alone does not give that."""
-    per = 8 if dtype is torch.bfloat16 else 4
+    per = 8 if dtype is _BF16 else 4
     ld = (cols + per - 1) // per * per
     return _empty((rows, cols), (ld, 1), dtype, idx, stream), ld
 
 
-def _rows(t: torch.Tensor, what: str, *dtypes: torch.dtype) -> tuple:
-    """(rows, columns, row stride) of a 2-D row-major tensor of one of these types.
-    A single row's stride is never used, and torch may leave any: it stands at a
-    16-byte multiple that covers the row."""
-    if t.dtype not in dtypes or t.dim() != 2:
-        raise ValueError(f"{what} must be a row-major 2-D tensor of {' or '.join(map(str, dtypes))}, got {t.dim()}-D {t.dtype}")
+def _rows(t: torch.Tensor, what: str, dtype: torch.dtype, other: Optional[torch.dtype] = None) -> tuple:
+    """(rows, columns, row stride) of a 2-D row-major tensor of this type (or the
+    other).  A single row's stride is never used, and torch may leave any: it
+    stands at a 16-byte multiple that covers the row."""
+    kind = t.dtype
+    if (kind is not dtype and kind is not other) or t.dim() != 2:
+        names = dtype if other is None else f"{dtype} or {other}"
+        raise ValueError(f"{what} must be a row-major 2-D tensor of {names}, got {t.dim()}-D {kind}")
     rows, cols = t.shape
     ld, step = t.stride()
     if step != 1 and cols > 1:
@@ -642,7 +647,7 @@ def _b_rows(b: torch.Tensor, what: str, dtype: torch.dtype, grouped: bool) -> tu
 def _scales_ready(t: torch.Tensor, name: str, what: str, rows: int, K: int, groups: int = 1) -> int:
     """Checks the GEMM-ready scales of `groups` operands of rows x K; returns the pointer."""
     need = groups * ((rows + 127) // 128) * ((K // 32 + 3) // 4) * 512
-    if t.dtype != torch.uint8 or t.dim() != 1 or t.numel() < need or not t.is_contiguous():
+    if t.dtype != _U8 or t.dim() != 1 or t.numel() < need or not t.is_contiguous():
         raise ValueError(f"{name}: {what} must be the GEMM-ready (SCALES_MMA) layout, a contiguous 1-D uint8 tensor of at "
                          f"least {need} bytes; got {t.dtype} {tuple(t.shape)} (quantize with scale_layout=SCALES_MMA or "
                          f"convert with mxfp4_scales_to_mma)")
@@ -653,8 +658,8 @@ def _gated(name: str, a_codes, a_scales, groups, b_codes, b_scales, K, alpha, li
     """The four gated entry points: z None or a tensor to write (forward), or the
     kept pre-activations (backward: keep_z is None)."""
     grouped, backward = groups is not None, keep_z is None
-    M, ka, lda = _rows(a_codes, "A", torch.uint8)
-    N, kb, ldb = _b_rows(b_codes, name, torch.uint8, grouped)
+    M, ka, lda = _rows(a_codes, "A", _U8)
+    N, kb, ldb = _b_rows(b_codes, name, _U8, grouped)
     if 2 * ka < K or 2 * kb < K:
         raise ValueError(f"{name}: codes hold {2 * min(ka, kb)} elements per row, K = {K}")
     G = _groups(name, *groups, b_codes) if grouped else 1
@@ -665,16 +670,16 @@ def _gated(name: str, a_codes, a_scales, groups, b_codes, b_scales, K, alpha, li
     ocols, zcols = (2 * N, 2 * N) if backward else (N // 2, N)
     pz, ldz = None, 0
     if z is not None:
-        pz, ldz = z.data_ptr(), _rows_of(z, "z", torch.bfloat16, M, zcols)
+        pz, ldz = z.data_ptr(), _rows_of(z, "z", _BF16, M, zcols)
         _device(name, stream, a_codes, z)
     if out is not None:
-        ldo = _rows_of(out, "out", torch.bfloat16, M, ocols)
+        ldo = _rows_of(out, "out", _BF16, M, ocols)
         _device(name, stream, a_codes, out)
     idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales)
     if out is None:
-        out, ldo = _empty_rows(M, ocols, torch.bfloat16, idx, stream)
+        out, ldo = _empty_rows(M, ocols, _BF16, idx, stream)
     if keep_z and z is None:
-        z, ldz = _empty_rows(M, zcols, torch.bfloat16, idx, stream)
+        z, ldz = _empty_rows(M, zcols, _BF16, idx, stream)
         pz = z.data_ptr()
     act_and_out = (alpha, limit, beta, pz, ldz, out.data_ptr(), ldo) if backward else \
         (alpha, limit, beta, out.data_ptr(), ldo, pz, ldz)
@@ -744,15 +749,15 @@ def mxfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Quantized] = None, st
     """Signed 8-bit codes and one scale per row of a 2-D bf16 tensor: activations
     by token, a weight [N, K] by output channel (see mxfp4_int8_quantize in
     include/mxfp4.h)."""
-    rows, cols, ld = _rows(x, "x", torch.bfloat16)
+    rows, cols, ld = _rows(x, "x", _BF16)
     if out is None:
         idx = _device("mxfp4_int8_quantize", stream, x)
-        codes = _empty((rows, cols), (cols, 1), torch.int8, idx, stream)
-        scales = _empty((rows,), (1,), torch.float32, idx, stream)
+        codes = _empty((rows, cols), (cols, 1), _I8, idx, stream)
+        scales = _empty((rows,), (1,), _F32, idx, stream)
         ldc, out = cols, Int8Quantized(codes, scales)
     else:
         codes, scales = out.codes, out.scales
-        ldc = _rows_of(codes, "out.codes", torch.int8, rows, cols)
+        ldc = _rows_of(codes, "out.codes", _I8, rows, cols)
         _token_scales(scales, "out.scales", (rows,))
         idx = _device("mxfp4_int8_quantize", stream, x, codes, scales)
     _run((_lib or lib()).mxfp4_int8_quantize, "mxfp4_int8_quantize", idx, stream, x.data_ptr(), rows, cols, ld,
@@ -761,15 +766,15 @@ def mxfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Quantized] = None, st
 
 
 def _token_scales(t: torch.Tensor, what: str, shape: tuple) -> int:
-    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+    if t.dtype != _F32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous float32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _int8_gemm(name: str, a_codes, a_scales, groups, b_codes, b_scales, out_dtype, out, stream) -> torch.Tensor:
     grouped = groups is not None
-    M, K, lda = _rows(a_codes, "A", torch.int8)
-    N, kb, ldb = _b_rows(b_codes, name, torch.int8, grouped)
+    M, K, lda = _rows(a_codes, "A", _I8)
+    N, kb, ldb = _b_rows(b_codes, name, _I8, grouped)
     if kb != K:
         raise ValueError(f"{name}: A has K = {K}, B {kb}")
     G = _groups(name, *groups, b_codes) if grouped else 1
@@ -777,7 +782,7 @@ def _int8_gemm(name: str, a_codes, a_scales, groups, b_codes, b_scales, out_dtyp
     psb = _token_scales(b_scales, "b_scales", (G, N) if grouped else (N,))
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+    if out_dtype is not _BF16 and out_dtype is not _F32:
         raise ValueError(f"{name}: the output must be bfloat16 or float32, got out_dtype {out_dtype}")
     if out is None:
         idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales)
@@ -785,7 +790,7 @@ def _int8_gemm(name: str, a_codes, a_scales, groups, b_codes, b_scales, out_dtyp
     else:
         ldo = _rows_of(out, "out", out_dtype, M, N)
         idx = _device(name, stream, a_codes, a_scales, b_codes, b_scales, out)
-    kind = OUT_F32 if out_dtype is torch.float32 else OUT_BF16
+    kind = OUT_F32 if out_dtype is _F32 else OUT_BF16
     fn = getattr(_lib or lib(), name)
     if grouped:
         _device(name, stream, a_codes, *groups)
@@ -822,7 +827,7 @@ def mxfp4_dropout(x: torch.Tensor, p: float, seed: int, elem_offset: int = 0, re
     from the Philox stream of (seed, element index) and never stored (see
     mxfp4_dropout in include/mxfp4.h).  The gradient is the same call on dY.
     out may be x or residual itself."""
-    rows, cols, ld = _rows(x, "x", torch.bfloat16, torch.float32)
+    rows, cols, ld = _rows(x, "x", _BF16, _F32)
     kind = x.dtype
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be within [0, 1], got {p}")
@@ -839,7 +844,7 @@ def mxfp4_dropout(x: torch.Tensor, p: float, seed: int, elem_offset: int = 0, re
         ldo = _rows_of(out, "out", kind, rows, cols)
         _device("mxfp4_dropout", stream, x, out)
     _run((_lib or lib()).mxfp4_dropout, "mxfp4_dropout", idx, stream, x.data_ptr(), ld, pr, ldr, rows, cols,
-         OUT_F32 if kind is torch.float32 else OUT_BF16, p, seed & 0xFFFFFFFFFFFFFFFF, elem_offset, out.data_ptr(), ldo)
+         OUT_F32 if kind is _F32 else OUT_BF16, p, seed & 0xFFFFFFFFFFFFFFFF, elem_offset, out.data_ptr(), ldo)
     return out
 
 
