@@ -129,8 +129,8 @@ using NvCfg = TileCfg<192, 5, 1, KIND_NV>;
 // warps 41.2).
 using GatedCfg = TileCfg<192, 3, 2, KIND_MX, 1, 8>;
 using BwdCfg = TileCfg<192, 5, 1, KIND_MX, 2, 8>;
-// Dense calls take 128-column tiles where those finish in clearly fewer rounds
-// of tiles (launch_dense): 256 x 5760 x 2880 8.0 against 9.1 us, 768 rows 11.5
+// Calls take 128-column tiles where those finish in clearly fewer rounds of
+// tiles (launch_tiles): 256 x 5760 x 2880 8.0 against 9.1 us, 768 rows 11.5
 // against 13.0; backward, 768 x 2880 x 2880, 12.4 against 14.1.
 using GatedNarrowCfg = TileCfg<128, 3, 2, KIND_MX, 2, 8>;
 using BwdNarrowCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8>;
@@ -144,6 +144,7 @@ using BwdNarrowCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8>;
 using I8Cfg = TileCfg<256, 6, 1, KIND_I8>;
 using I8NarrowCfg = TileCfg<128, 8, 1, KIND_I8>;
 using I8GroupedCfg = TileCfg<256, 5, 1, KIND_I8>;   // the group table takes 4 KB of shared memory
+using I8GroupedNarrowCfg = TileCfg<128, 7, 1, KIND_I8>;
 
 __device__ unsigned int g_error_code;
 
@@ -1280,15 +1281,18 @@ int launch_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scal
     return launch_cfg<NvCfg, MODE_DENSE>(g, s);
 }
 
-// Dense launch with the wide or the narrow tile: a narrow tile costs 0.65 to 0.8
-// of a wide one (its instructions are shorter, its operand bytes per product
-// more), so it has to save that much in rounds of the resident pairs.
-template <class Wide, class Narrow, int OUT>
-static int launch_dense(const GemmArgs &g, cudaStream_t s) {
-    const int64_t pairs = sm_count() / 2, tiles_m = (g.M + 255) / 256;
+// Launch with the wide or the narrow tile: a narrow tile costs 0.65 to 0.8 of a
+// wide one (its instructions are shorter, its operand bytes per product more),
+// so it has to save that much in rounds of the resident pairs.  The row tiles of
+// groups are on the device: their number is taken as that of all rows and a
+// quarter per group (half a tile for every other group, whose rows end in the
+// first half of one).
+template <class Wide, class Narrow, int MODE, int OUT>
+static int launch_tiles(const GemmArgs &g, cudaStream_t s) {
+    const int64_t pairs = sm_count() / 2, tiles_m = (g.M + 255) / 256 + (MODE == MODE_GROUPED_M ? g.G / 4 : 0);
     auto rounds = [&](int64_t bn) { return (tiles_m * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
-    if (4 * rounds(Narrow::BN) < 5 * rounds(Wide::BN)) return launch_cfg<Narrow, MODE_DENSE, OUT>(g, s);
-    return launch_cfg<Wide, MODE_DENSE, OUT>(g, s);
+    if (4 * rounds(Narrow::BN) < 5 * rounds(Wide::BN)) return launch_cfg<Narrow, MODE, OUT>(g, s);
+    return launch_cfg<Wide, MODE, OUT>(g, s);
 }
 
 // Gated products: the activation of column pairs of A B^T (forward), or dz from
@@ -1303,10 +1307,10 @@ int launch_gated(const GatedArgs &a, cudaStream_t s) {
     g.limit = a.limit;
     g.beta = a.beta;
     if (a.backward)
-        return a.offsets ? launch_cfg<BwdCfg, MODE_GROUPED_M, OUT_GATED_BWD>(g, s)
-                         : launch_dense<BwdCfg, BwdNarrowCfg, OUT_GATED_BWD>(g, s);
-    return a.offsets ? launch_cfg<GatedCfg, MODE_GROUPED_M, OUT_GATED>(g, s)
-                     : launch_dense<GatedCfg, GatedNarrowCfg, OUT_GATED>(g, s);
+        return a.offsets ? launch_tiles<BwdCfg, BwdNarrowCfg, MODE_GROUPED_M, OUT_GATED_BWD>(g, s)
+                         : launch_tiles<BwdCfg, BwdNarrowCfg, MODE_DENSE, OUT_GATED_BWD>(g, s);
+    return a.offsets ? launch_tiles<GatedCfg, GatedNarrowCfg, MODE_GROUPED_M, OUT_GATED>(g, s)
+                     : launch_tiles<GatedCfg, GatedNarrowCfg, MODE_DENSE, OUT_GATED>(g, s);
 }
 
 int launch_int8_gemm(const Int8Args &a, cudaStream_t s) {
@@ -1316,9 +1320,10 @@ int launch_int8_gemm(const Int8Args &a, cudaStream_t s) {
     g.a_tok = a.a_scales;
     g.b_chan = a.b_scales;
     if (a.offsets)
-        return a.bf16 ? launch_cfg<I8GroupedCfg, MODE_GROUPED_M, OUT_BF16>(g, s)
-                      : launch_cfg<I8GroupedCfg, MODE_GROUPED_M, OUT_F32>(g, s);
-    return a.bf16 ? launch_dense<I8Cfg, I8NarrowCfg, OUT_BF16>(g, s) : launch_dense<I8Cfg, I8NarrowCfg, OUT_F32>(g, s);
+        return a.bf16 ? launch_tiles<I8GroupedCfg, I8GroupedNarrowCfg, MODE_GROUPED_M, OUT_BF16>(g, s)
+                      : launch_tiles<I8GroupedCfg, I8GroupedNarrowCfg, MODE_GROUPED_M, OUT_F32>(g, s);
+    return a.bf16 ? launch_tiles<I8Cfg, I8NarrowCfg, MODE_DENSE, OUT_BF16>(g, s)
+                  : launch_tiles<I8Cfg, I8NarrowCfg, MODE_DENSE, OUT_F32>(g, s);
 }
 
 int get_error(cudaStream_t s) {

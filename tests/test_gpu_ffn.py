@@ -136,7 +136,7 @@ def test_gated_gemm_large_and_tiny_values(M):
 
 
 @pytest.mark.parametrize("sizes,I,K", [([1, 130, 0, 257, 128], 96, 256), ([300, 5, 64], 200, 576), ([0, 0, 17], 8, 64),
-                                       ([33] * 40, 48, 128)])
+                                       ([33] * 40, 48, 128), ([700, 900, 0, 100], 2880, 64)])
 @pytest.mark.parametrize("keep", [False, True])
 def test_grouped_gated_gemm(sizes, I, K, keep):
     c = grouped_operands(sizes, 2 * I, K, 11, 1.0, 0.2, slack=1)
@@ -256,7 +256,7 @@ def test_gated_backward_strided_and_nan():
 
 
 @pytest.mark.parametrize("sizes,I,K", [([1, 130, 0, 257, 128], 96, 256), ([300, 5, 64], 200, 576), ([0, 17], 8, 64),
-                                       ([33] * 40, 52, 128), ([700, 400], 1000, 64)])
+                                       ([33] * 40, 52, 128), ([700, 400], 1000, 64), ([700, 900, 0, 100], 2880, 64)])
 def test_grouped_gated_backward(sizes, I, K):
     c = grouped_operands(sizes, I, K, 51, 1e-2, 0.1, slack=1)
     zb = z_values(c["rows"], I, 52)
@@ -421,7 +421,7 @@ def test_int8_gemm_nan_scales_and_strides():
 
 
 @pytest.mark.parametrize("sizes,N,K", [([1, 130, 0, 257, 128], 192, 256), ([300, 5, 64], 260, 528), ([0, 17], 8, 16),
-                                       ([33] * 40, 72, 144), ([2, 0, 1, 1], 2880, 1440)])
+                                       ([33] * 40, 72, 144), ([2, 0, 1, 1], 2880, 1440), ([700, 900, 0, 100], 2880, 80)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_int8_grouped_gemm(sizes, N, K, dtype):
     G = len(sizes)
