@@ -32,16 +32,12 @@ __host__ __device__ __forceinline__ int64_t mma_scale_off(int64_t row, int64_t k
 // ---------------------------------------------------------------------------
 struct U4 { uint32_t x, y, z, w; };
 
-// Rounds FIRST .. 9; (k0, k1) is the key itself.
-template <int FIRST>
-__device__ __forceinline__ U4 philox_rounds(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3,
+__device__ __forceinline__ U4 philox4x32_10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3,
                                             uint32_t k0, uint32_t k1) {
     constexpr uint32_t M0 = 0xD2511F53u, M1 = 0xCD9E8D57u;
     constexpr uint32_t W0 = 0x9E3779B9u, W1 = 0xBB67AE85u;
-    k0 += FIRST * W0;
-    k1 += FIRST * W1;
 #pragma unroll
-    for (int r = FIRST; r < 10; ++r) {
+    for (int r = 0; r < 10; ++r) {
         const uint64_t p0 = (uint64_t)M0 * c0;   // one widening multiply each
         const uint64_t p1 = (uint64_t)M1 * c2;
         const uint32_t n0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
@@ -50,10 +46,6 @@ __device__ __forceinline__ U4 philox_rounds(uint32_t c0, uint32_t c1, uint32_t c
         k0 += W0; k1 += W1;
     }
     return U4{c0, c1, c2, c3};
-}
-__device__ __forceinline__ U4 philox4x32_10(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3,
-                                            uint32_t k0, uint32_t k1) {
-    return philox_rounds<0>(c0, c1, c2, c3, k0, k1);
 }
 
 // Sign mask of the RHT diagonal for a seed: word 0 of the block with counter
