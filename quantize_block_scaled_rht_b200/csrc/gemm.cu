@@ -62,8 +62,10 @@ constexpr int MAX_STAGES = 8;
 // epilogues with real arithmetic: a warp may read only the quarter of the tensor
 // memory lanes that its index selects, so two warps share a quarter and take
 // its column steps in turn.
+// SUB: if not 0, the tiles of the last, partial round are cut into pieces of SUB
+// columns (get_item).
 constexpr int KIND_MX = 0, KIND_NV = 1, KIND_I8 = 2;
-template <int BN_, int STAGES_, int KCH_, int KIND_ = KIND_MX, int EPI_BUFS_ = 2, int EPI_WARPS_ = 4>
+template <int BN_, int STAGES_, int KCH_, int KIND_ = KIND_MX, int EPI_BUFS_ = 2, int EPI_WARPS_ = 4, int SUB_ = 0>
 struct TileCfg {
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
@@ -73,6 +75,8 @@ struct TileCfg {
     static constexpr int EPI_WARPS = EPI_WARPS_;
     static constexpr int SPLIT = EPI_WARPS / 4;       // warps per lane quarter
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int SUB = SUB_;
+    static constexpr int PIECES = SUB ? BN / SUB : 1;
     static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * EPI_BUF;
     static constexpr int KPB = I8 ? 1 : 2;            // K-elements per byte
     static constexpr int KMMA = 32 * KPB;             // K-elements per instruction (32 bytes)
@@ -105,6 +109,7 @@ struct TileCfg {
     static_assert(BN == 128 || BN == 192 || (I8 && BN == 256), "tile width");
     static_assert(KCH == 1 || KCH == 2, "chunks per stage");
     static_assert(EPI_WARPS == 4 || EPI_WARPS == 8, "epilogue warps");
+    static_assert(SUB == 0 || (SUB == 64 && BN % 64 == 0 && !I8), "pieces start on an even 32-column scale group");
     static_assert(STAGES <= MAX_STAGES, "stages");
     static_assert(SF_COL + 2 * SF_STAGE_COLS <= ACC1_COL, "TMEM layout");
     static_assert(A_CHUNK % 1024 == 0 && B_CHUNK % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle alignment");
@@ -134,6 +139,15 @@ using BwdCfg = TileCfg<192, 5, 1, KIND_MX, 2, 8>;
 // against 13.0; backward, 768 x 2880 x 2880, 12.4 against 14.1.
 using GatedNarrowCfg = TileCfg<128, 3, 2, KIND_MX, 2, 8>;
 using BwdNarrowCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8>;
+// The backward epilogue outlasts the MMAs, so a last round that only a few pairs
+// take part in costs a whole tile's epilogue.  A dense call whose last round
+// still fits one round in 64-column pieces takes the form that cuts it (launch_cut):
+// 4096 x 2880 x 2880 34.5 against 36.9 us (K = 64: 26.8 against 29.1), 16 rows
+// 9.5 against 10.4, 1024 x 1024 x 1024 7.6 against 8.6.  The counting costs calls
+// that cut nothing 1 to 3%, so they, and the grouped calls, whose number of tiles
+// the host does not know, have the plain form.
+using BwdCutCfg = TileCfg<192, 5, 1, KIND_MX, 2, 8, 64>;
+using BwdNarrowCutCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8, 64>;
 // int8: without scale factors in tensor memory two 256-column accumulators fit,
 // and a 256 x 256 tile reads 1/8 fewer operand bytes per product than 256 x 192
 // (4096 x 2880 x 2880: 28.6 us, 256 x 192 33.8, and 31.7 with the ring as 3 x 256
@@ -225,6 +239,7 @@ struct TileInfo {
     int64_t sfb_rt_base;  // first 128-row scale tile of this B operand (expert)
     int64_t k0;         // first K element of the tile's reduction (grouped K: the group's offset)
     int64_t kg;         // K elements of the reduction
+    int width;          // columns (get_item)
 };
 
 // Kernel modes: dense; grouped rows (per-expert row ranges of A, one B per
@@ -284,6 +299,23 @@ __device__ __forceinline__ TileInfo get_tile(int t, uint32_t rank, const GemmPar
         ti.c_row0 = ti.row0;
     }
     return ti;
+}
+
+// Work item t: pair tile t up to `whole`, then the tiles after it in PIECES
+// pieces of SUB columns each.
+template <class Cfg, int MODE>
+__device__ __forceinline__ TileInfo get_item(int t, int whole, uint32_t rank, const GemmParams &p, const int *cum,
+                                             int tiles_n, int &g_at) {
+    if constexpr (Cfg::SUB == 0) {
+        return get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n, g_at);
+    } else {
+        const int piece = t < whole ? 0 : (t - whole) % Cfg::PIECES;
+        TileInfo ti = get_tile<Cfg::BN, MODE>(t < whole ? t : whole + (t - whole) / Cfg::PIECES, rank, p, cum, tiles_n, g_at);
+        ti.n0 += Cfg::SUB * piece;
+        ti.b_row += Cfg::SUB * piece;
+        ti.width = t < whole ? Cfg::BN : Cfg::SUB;
+        return ti;
+    }
 }
 
 // int8 epilogue: 32 integer sums of one row to (sum * token scale) * channel
@@ -384,10 +416,10 @@ struct ZRing {
     __device__ __forceinline__ void start(int t0, int part) { t = t0; j = part; g_at = 0; issued = used = 0; }
     // Issue loads up to the box after the current one.
     __device__ __forceinline__ void fill(const CUtensorMap *map, uint8_t *bufs, uint64_t *bars, const GemmParams &p,
-                                         const int *cum, int tiles_n, int ntiles, int npairs, uint32_t rank,
+                                         const int *cum, int tiles_n, int ntiles, int whole, int npairs, uint32_t rank,
                                          int row_lo, int lane, int part) {
         while (issued < used + 2 && t < ntiles) {
-            if (j == part) ti = get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n, g_at);
+            if (j == part) ti = get_item<Cfg, MODE>(t, whole, rank, p, cum, tiles_n, g_at);
             const bool boxes = row_lo < ti.rows_valid && (MODE == MODE_DENSE || row_lo + 32 <= ti.rows_valid);
             const int64_t col0 = ti.n0 + 32 * j;
             if (boxes && col0 < p.N && !ragged_box(2 * col0, 64, 2 * p.N, 2)) {
@@ -400,7 +432,7 @@ struct ZRing {
                 ++issued;
             }
             j += Cfg::SPLIT;
-            if (!boxes || j >= Cfg::BN / 32) { j = part; t += npairs; }
+            if (!boxes || j >= (Cfg::SUB ? ti.width : Cfg::BN) / 32) { j = part; t += npairs; }
         }
         __syncwarp();
     }
@@ -414,7 +446,7 @@ struct ZRing {
 // 32-element blocks per MMA); k >> 1 steps to the next 4-block atom.
 template <class Cfg, int NATOMS, int NK>
 __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint32_t st, uint32_t sfa_col, uint32_t b_shift,
-                                            bool first) {
+                                            bool first, uint32_t desc = Cfg::IDESC) {
     constexpr int NRT = Cfg::NRT, NATOM = Cfg::NATOM;
     if constexpr (Cfg::I8) {
         const uint64_t adesc = smem_desc(st, 16, 1024, 2);
@@ -448,7 +480,7 @@ __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint32_t st, uint32
             mma_nvf4_pair_elect(d_tmem, adesc + a_off, bdesc + b_off, Cfg::IDESC, sfa_col + 4u * (uint32_t)k,
                                 sfb_col + 4u * NRT * (uint32_t)k + b_shift, (k == 0 && first) ? 0u : 1u);
         } else {
-            const uint32_t idesc = (k & 1) ? (Cfg::IDESC | (2u << 29) | (2u << 4)) : Cfg::IDESC;
+            const uint32_t idesc = (k & 1) ? (desc | (2u << 29) | (2u << 4)) : desc;
             mma_mxf4_pair_elect(d_tmem, adesc + a_off, bdesc + b_off, idesc, sfa_col + 4u * (uint32_t)(k >> 1),
                                 sfb_col + 4u * NRT * (uint32_t)(k >> 1) + b_shift, (k == 0 && first) ? 0u : 1u);
         }
@@ -459,7 +491,7 @@ __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint32_t st, uint32
 // KMMA) MMAs (kleft / 64 for E2M1) and ceil(NK / 2) scale atoms.
 template <class Cfg>
 __device__ __noinline__ void issue_stage_tail(uint32_t d_tmem, uint32_t st, uint32_t sfa_col, uint32_t b_shift,
-                                              bool first, int nk) {
+                                              bool first, int nk, uint32_t desc) {
     if constexpr (Cfg::NV) {                  // one atom per MMA; a stage holds 4 * KCH MMAs
         switch (nk) {
             case 1: issue_stage<Cfg, 1, 1>(d_tmem, st, sfa_col, b_shift, first); break;
@@ -470,13 +502,13 @@ __device__ __noinline__ void issue_stage_tail(uint32_t d_tmem, uint32_t st, uint
         return;
     }
     switch (nk) {
-        case 1: issue_stage<Cfg, 1, 1>(d_tmem, st, sfa_col, b_shift, first); break;
-        case 2: issue_stage<Cfg, 1, 2>(d_tmem, st, sfa_col, b_shift, first); break;
-        case 3: issue_stage<Cfg, 2, 3>(d_tmem, st, sfa_col, b_shift, first); break;
-        case 4: issue_stage<Cfg, 2, 4>(d_tmem, st, sfa_col, b_shift, first); break;
-        case 5: issue_stage<Cfg, 3, 5>(d_tmem, st, sfa_col, b_shift, first); break;
-        case 6: issue_stage<Cfg, 3, 6>(d_tmem, st, sfa_col, b_shift, first); break;
-        case 7: issue_stage<Cfg, 4, 7>(d_tmem, st, sfa_col, b_shift, first); break;
+        case 1: issue_stage<Cfg, 1, 1>(d_tmem, st, sfa_col, b_shift, first, desc); break;
+        case 2: issue_stage<Cfg, 1, 2>(d_tmem, st, sfa_col, b_shift, first, desc); break;
+        case 3: issue_stage<Cfg, 2, 3>(d_tmem, st, sfa_col, b_shift, first, desc); break;
+        case 4: issue_stage<Cfg, 2, 4>(d_tmem, st, sfa_col, b_shift, first, desc); break;
+        case 5: issue_stage<Cfg, 3, 5>(d_tmem, st, sfa_col, b_shift, first, desc); break;
+        case 6: issue_stage<Cfg, 3, 6>(d_tmem, st, sfa_col, b_shift, first, desc); break;
+        case 7: issue_stage<Cfg, 4, 7>(d_tmem, st, sfa_col, b_shift, first, desc); break;
         default: break;   // a full stage never takes this path
     }
 }
@@ -587,7 +619,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
-    const int ntiles = sh->ntiles;
+    // work items: the tiles, with SUB those of the partial last round in pieces
+    int ntiles = sh->ntiles, whole = ntiles;
+    if constexpr (Cfg::SUB != 0) {
+        const int rest = ntiles % npairs;
+        whole = ntiles - rest;
+        ntiles = whole + rest * Cfg::PIECES;
+    }
     bool aborted_any = false;
 
     if (warp == 0) {
@@ -599,7 +637,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             int s = 0, g_at = 0;
             uint32_t ph = 0;
             for (int t = pair; t < ntiles && !sh->abort; t += npairs) {
-                const TileInfo ti = get_tile<BN, MODE>(t, rank, p, cum, tiles_n, g_at);
+                const TileInfo ti = get_item<Cfg, MODE>(t, whole, rank, p, cum, tiles_n, g_at);
+                const int half_b = (Cfg::SUB ? ti.width : BN) / 2;   // rows of B of this CTA (a box may load more)
                 const int32_t sfa_rt = (int32_t)(ti.row0 / 128);
                 const int32_t sfb_rt = (int32_t)(ti.sfb_rt_base + ti.n0 / 128);
                 const int ktiles = ktiles_of(ti);
@@ -622,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                             if (MODE != MODE_DENSE || rank == 0 || p.M > BM)
                                 tma_load_2d_pair(st + c * Cfg::A_CHUNK, &tma_a, kx, (int32_t)ti.row0, full_leader);
                             tma_load_2d_pair(st + A_BYTES + c * Cfg::B_CHUNK, &tma_b, kx,
-                                             (int32_t)(ti.b_row + rank * (BN / 2)), full_leader);
+                                             (int32_t)(ti.b_row + rank * half_b), full_leader);
                         }
                         // scale atoms: NATOM consecutive K atoms of one (A) or NRT (B) 128-row tiles
                         if constexpr (!Cfg::I8) {
@@ -658,7 +697,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             int acc = 0, g_at = 0;
             uint32_t acc_ph = 0;
             for (int t = pair; t < ntiles && !sh->abort; t += npairs) {
-                const TileInfo ti = get_tile<BN, MODE>(t, 0, p, cum, tiles_n, g_at);
+                const TileInfo ti = get_item<Cfg, MODE>(t, whole, 0, p, cum, tiles_n, g_at);
+                uint32_t desc = Cfg::IDESC;
+                if constexpr (Cfg::SUB != 0) desc = (desc & ~(63u << 17)) | ((uint32_t)(ti.width >> 3) << 17);
                 const int64_t rt0 = ti.n0 / 128;
                 const uint32_t b_shift = (uint32_t)((ti.n0 - rt0 * 128) / 32);
                 if (!wait_phase(&sh->tmem_empty[acc], acc_ph ^ 1u, sh, limit)) break;
@@ -675,10 +716,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     // a stage whose last instruction is partial (int8, K not a
                     // multiple of 32) is full too: TMA filled it up with zeros
                     if (kleft > Cfg::KSTEP - Cfg::KMMA)
-                        issue_stage<Cfg, NATOM, 4 * KCH>(d_tmem, st, sfa_col, b_shift, kt == 0);
+                        issue_stage<Cfg, NATOM, 4 * KCH>(d_tmem, st, sfa_col, b_shift, kt == 0, desc);
                     else
                         issue_stage_tail<Cfg>(d_tmem, st, sfa_col, b_shift, kt == 0,
-                                              (int)((kleft + Cfg::KMMA - 1) / Cfg::KMMA));
+                                              (int)((kleft + Cfg::KMMA - 1) / Cfg::KMMA), desc);
                     issued = true;
                     tc_commit_pair_elect(&sh->empty[s]);
                     ++kglobal;
@@ -715,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         ring.start(pair, part);
         int g_at = 0;
         for (int t = pair; t < ntiles; t += npairs) {
-            const TileInfo ti = get_tile<BN, MODE>(t, rank, p, cum, tiles_n, g_at);
+            const TileInfo ti = get_item<Cfg, MODE>(t, whole, rank, p, cum, tiles_n, g_at);
             const int row_lo = 32 * q;
             // int8: this lane's token scale, and the channel scale of column
             // 32 j + lane of the tile, one 32-column step ahead
@@ -729,7 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 chan = load_chan(0);
             }
             if constexpr (OUT == OUT_GATED_BWD)
-                ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
+                ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, whole, npairs, rank, row_lo, lane, part);
             // one answer for the warp: what follows needs it whole
             if (!__all_sync(0xFFFFFFFFu, wait_phase(&sh->tmem_full[acc], acc_ph, sh, limit))) break;
             tc_fence_after();
@@ -841,7 +882,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 const GatedAct act{p.act_alpha, p.act_limit, p.act_beta};
                 const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16) + (acc ? Cfg::ACC1_COL : 0u);
                 bool ok = true;
-                for (int j = part; j < BN / 32; j += Cfg::SPLIT) {
+                const int steps = (Cfg::SUB ? ti.width : BN) / 32;
+                for (int j = part; j < steps; j += Cfg::SPLIT) {
                     uint32_t v[32], w[32];
                     tmem_ld_32x32b_x32(tm + 32u * j, v);
                     // z arrives while the accumulators do
@@ -853,7 +895,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     const uint32_t b = ring.used & 1u;
                     uint8_t *buf = ring_bufs + b * EPI_BUF;
                     if (in_ring) {
-                        ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
+                        ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, whole, npairs, rank, row_lo, lane, part);
                         // one answer for the warp: the tensor memory instructions need it whole
                         ok = __all_sync(0xFFFFFFFFu, wait_phase(&ring_bars[b], (ring.used >> 1) & 1u, sh, limit));
                         if (ok) unstage_row128(smem_u32(buf), lane, w);
@@ -865,7 +907,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     }
                     __syncwarp();
                     tmem_ld_wait_x32(v);
-                    if (j + Cfg::SPLIT >= BN / 32) {
+                    if (j + Cfg::SPLIT >= steps) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
@@ -1215,7 +1257,7 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     int pairs = pairs_max;
     if (MODE != MODE_GROUPED_M) {
         const int64_t tiles = (MODE == MODE_GROUPED_K ? g.G : 1) * ((g.M + 255) / 256) * ((g.N + BN - 1) / BN);
-        pairs = (int)(tiles < pairs_max ? tiles : pairs_max);
+        pairs = (int)(tiles * Cfg::PIECES < pairs_max ? tiles * Cfg::PIECES : pairs_max);
     }
     const cudaError_t e = launch_pdl(mxfp4_gemm_kernel<Cfg, MODE, OUT>, dim3((unsigned)(2 * pairs)), dim3(Cfg::THREADS),
                                      (size_t)Cfg::SMEM_BYTES, s, ta, tb, tc, tsa, tsb, tz, p);
@@ -1281,18 +1323,30 @@ int launch_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scal
     return launch_cfg<NvCfg, MODE_DENSE>(g, s);
 }
 
+// Launch with the last round of tiles cut into pieces where those fit one round.
+template <class Cfg, class Cut, int MODE, int OUT>
+static int launch_cut(const GemmArgs &g, cudaStream_t s) {
+    if constexpr (Cut::SUB != 0) {
+        static_assert(MODE == MODE_DENSE && Cut::BN == Cfg::BN, "the same tiles, counted on the host");
+        const int64_t pairs = sm_count() / 2, rest = ((g.M + 255) / 256) * ((g.N + Cfg::BN - 1) / Cfg::BN) % pairs;
+        if (rest && rest * Cut::PIECES <= pairs) return launch_cfg<Cut, MODE, OUT>(g, s);
+    }
+    return launch_cfg<Cfg, MODE, OUT>(g, s);
+}
+
 // Launch with the wide or the narrow tile: a narrow tile costs 0.65 to 0.8 of a
 // wide one (its instructions are shorter, its operand bytes per product more),
 // so it has to save that much in rounds of the resident pairs.  The row tiles of
 // groups are on the device: their number is taken as that of all rows and a
 // quarter per group (half a tile for every other group, whose rows end in the
 // first half of one).
-template <class Wide, class Narrow, int MODE, int OUT>
+// WideCut, NarrowCut: the same tiles with the last round cut into pieces.
+template <class Wide, class Narrow, int MODE, int OUT, class WideCut = Wide, class NarrowCut = Narrow>
 static int launch_tiles(const GemmArgs &g, cudaStream_t s) {
     const int64_t pairs = sm_count() / 2, tiles_m = (g.M + 255) / 256 + (MODE == MODE_GROUPED_M ? g.G / 4 : 0);
     auto rounds = [&](int64_t bn) { return (tiles_m * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
-    if (4 * rounds(Narrow::BN) < 5 * rounds(Wide::BN)) return launch_cfg<Narrow, MODE, OUT>(g, s);
-    return launch_cfg<Wide, MODE, OUT>(g, s);
+    if (4 * rounds(Narrow::BN) < 5 * rounds(Wide::BN)) return launch_cut<Narrow, NarrowCut, MODE, OUT>(g, s);
+    return launch_cut<Wide, WideCut, MODE, OUT>(g, s);
 }
 
 // Gated products: the activation of column pairs of A B^T (forward), or dz from
@@ -1308,7 +1362,7 @@ int launch_gated(const GatedArgs &a, cudaStream_t s) {
     g.beta = a.beta;
     if (a.backward)
         return a.offsets ? launch_tiles<BwdCfg, BwdNarrowCfg, MODE_GROUPED_M, OUT_GATED_BWD>(g, s)
-                         : launch_tiles<BwdCfg, BwdNarrowCfg, MODE_DENSE, OUT_GATED_BWD>(g, s);
+                         : launch_tiles<BwdCfg, BwdNarrowCfg, MODE_DENSE, OUT_GATED_BWD, BwdCutCfg, BwdNarrowCutCfg>(g, s);
     return a.offsets ? launch_tiles<GatedCfg, GatedNarrowCfg, MODE_GROUPED_M, OUT_GATED>(g, s)
                      : launch_tiles<GatedCfg, GatedNarrowCfg, MODE_DENSE, OUT_GATED>(g, s);
 }

@@ -207,6 +207,13 @@ def test_gated_backward(M, I, K, act):
     assert again is z and torch.equal(z, dz)
 
 
+@pytest.mark.parametrize("M,I,K", [(3500, 1344, 64), (3400, 1332, 192), (23000, 100, 64), (4000, 12, 576), (300, 1152, 320)])
+def test_gated_backward_last_round_in_pieces(M, I, K):
+    """Tiles of one or several rounds whose last is cut: both tile widths, pieces
+    that end inside their columns and ones past the last column."""
+    test_gated_backward(M, I, K, ffn.CLAMPED)
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_gated_backward_against_differences_of_the_forward(act):
     """dz against central differences of the 64-bit forward form, not its derivative."""
