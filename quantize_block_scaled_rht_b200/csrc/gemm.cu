@@ -109,7 +109,7 @@ struct TileCfg {
     static_assert(BN == 128 || BN == 192 || (I8 && BN == 256), "tile width");
     static_assert(KCH == 1 || KCH == 2, "chunks per stage");
     static_assert(EPI_WARPS == 4 || EPI_WARPS == 8, "epilogue warps");
-    static_assert(SUB == 0 || (SUB == 64 && BN % 64 == 0 && !I8), "pieces start on an even 32-column scale group");
+    static_assert(SUB == 0 || (BN % SUB == 0 && (SUB == 64 || (I8 && SUB == 128))), "pieces of a tile (E2M1: that start on an even 32-column scale group)");
     static_assert(STAGES <= MAX_STAGES, "stages");
     static_assert(SF_COL + 2 * SF_STAGE_COLS <= ACC1_COL, "TMEM layout");
     static_assert(A_CHUNK % 1024 == 0 && B_CHUNK % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle alignment");
@@ -142,8 +142,8 @@ using BwdNarrowCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8>;
 // The backward epilogue outlasts the MMAs, so a last round that only a few pairs
 // take part in costs a whole tile's epilogue.  A dense call whose last round
 // still fits one round in 64-column pieces takes the form that cuts it (launch_cut):
-// 4096 x 2880 x 2880 34.5 against 36.9 us (K = 64: 26.8 against 29.1), 16 rows
-// 9.5 against 10.4, 1024 x 1024 x 1024 7.6 against 8.6.  The counting costs calls
+// 4096 x 2880 x 2880 34.6 against 36.9 us (K = 64: 26.2 against 29.1), 16 rows
+// 9.2 against 10.4, 1024 x 1024 x 1024 7.3 against 8.6.  The counting costs calls
 // that cut nothing 1 to 3%, so they, and the grouped calls, whose number of tiles
 // the host does not know, have the plain form.
 using BwdCutCfg = TileCfg<192, 5, 1, KIND_MX, 2, 8, 64>;
@@ -157,6 +157,13 @@ using BwdNarrowCutCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8, 64>;
 // bytes win (1024 x 2880 x 2880: 13.8 against 16.4).
 using I8Cfg = TileCfg<256, 6, 1, KIND_I8>;
 using I8NarrowCfg = TileCfg<128, 8, 1, KIND_I8>;
+// The last round of a dense call in 128-column pieces, with B boxes of their
+// size, where those fit one round: 2048 x 2880 x 2880 18.4 against 19.8 us (96
+// tiles: a round of 74, then 14 tiles in two pieces and 8 of the last 64 columns in
+// one), 1024 x 5760 x 2880 18.2 against 19.5, 4096 x 2880 x 2880 25.7 against 27.2.
+// Narrow tiles in 64-column pieces: 512 x 1024 x 1024 6.3 against 6.6, but 16 x
+// 2880 x 2880 9.85 against 9.5; not kept.
+using I8CutCfg = TileCfg<256, 6, 1, KIND_I8, 2, 4, 128>;
 using I8GroupedCfg = TileCfg<256, 5, 1, KIND_I8>;   // the group table takes 4 KB of shared memory
 using I8GroupedNarrowCfg = TileCfg<128, 7, 1, KIND_I8>;
 
@@ -182,6 +189,9 @@ struct GemmParams {
     float act_alpha, act_limit, act_beta;
     int num_groups;
     uint32_t stage_tx;         // bytes of both CTAs' loads of one stage
+    // with TileCfg::SUB: tiles of the full rounds, then tiles in PIECES pieces each,
+    // then (int8) tiles of the last columns in as many as N needs; work items in all
+    int cut_whole, cut_tiles, cut_last, cut_items;
     uint64_t wait_limit_ns;
 };
 
@@ -301,19 +311,34 @@ __device__ __forceinline__ TileInfo get_tile(int t, uint32_t rank, const GemmPar
     return ti;
 }
 
-// Work item t: pair tile t up to `whole`, then the tiles after it in PIECES
-// pieces of SUB columns each.
+// Work item t: pair tile t in the full rounds; with SUB, the tiles of the last
+// round in pieces of SUB columns.  int8: tiles of the last columns have only the
+// pieces that N reaches.  The backward product, whose small pieces notice the
+// arithmetic (K = 64: 26.2 against 27.0 us), counts all and finds some empty.
 template <class Cfg, int MODE>
-__device__ __forceinline__ TileInfo get_item(int t, int whole, uint32_t rank, const GemmParams &p, const int *cum,
-                                             int tiles_n, int &g_at) {
+__device__ __forceinline__ TileInfo get_item(int t, uint32_t rank, const GemmParams &p, const int *cum, int tiles_n,
+                                             int &g_at) {
     if constexpr (Cfg::SUB == 0) {
         return get_tile<Cfg::BN, MODE>(t, rank, p, cum, tiles_n, g_at);
     } else {
-        const int piece = t < whole ? 0 : (t - whole) % Cfg::PIECES;
-        TileInfo ti = get_tile<Cfg::BN, MODE>(t < whole ? t : whole + (t - whole) / Cfg::PIECES, rank, p, cum, tiles_n, g_at);
+        int tile = t, piece = 0;
+        if (t >= p.cut_whole) {
+            const int u = t - p.cut_whole;
+            if (!Cfg::I8 || u < p.cut_tiles * Cfg::PIECES) {
+                tile = p.cut_whole + u / Cfg::PIECES;
+                piece = u % Cfg::PIECES;
+            } else {                            // first pieces of all, second pieces of all, ..
+                tile = t - p.cut_tiles * (Cfg::PIECES - 1);
+                while (tile >= p.cut_whole + p.cut_tiles + p.cut_last) {
+                    tile -= p.cut_last;
+                    ++piece;
+                }
+            }
+        }
+        TileInfo ti = get_tile<Cfg::BN, MODE>(tile, rank, p, cum, tiles_n, g_at);
         ti.n0 += Cfg::SUB * piece;
         ti.b_row += Cfg::SUB * piece;
-        ti.width = t < whole ? Cfg::BN : Cfg::SUB;
+        ti.width = t < p.cut_whole ? Cfg::BN : Cfg::SUB;
         return ti;
     }
 }
@@ -416,10 +441,10 @@ struct ZRing {
     __device__ __forceinline__ void start(int t0, int part) { t = t0; j = part; g_at = 0; issued = used = 0; }
     // Issue loads up to the box after the current one.
     __device__ __forceinline__ void fill(const CUtensorMap *map, uint8_t *bufs, uint64_t *bars, const GemmParams &p,
-                                         const int *cum, int tiles_n, int ntiles, int whole, int npairs, uint32_t rank,
+                                         const int *cum, int tiles_n, int ntiles, int npairs, uint32_t rank,
                                          int row_lo, int lane, int part) {
         while (issued < used + 2 && t < ntiles) {
-            if (j == part) ti = get_item<Cfg, MODE>(t, whole, rank, p, cum, tiles_n, g_at);
+            if (j == part) ti = get_item<Cfg, MODE>(t, rank, p, cum, tiles_n, g_at);
             const bool boxes = row_lo < ti.rows_valid && (MODE == MODE_DENSE || row_lo + 32 <= ti.rows_valid);
             const int64_t col0 = ti.n0 + 32 * j;
             if (boxes && col0 < p.N && !ragged_box(2 * col0, 64, 2 * p.N, 2)) {
@@ -455,7 +480,7 @@ __device__ __forceinline__ void issue_stage(uint32_t d_tmem, uint32_t st, uint32
         for (int k = 0; k < NK; ++k) {
             const uint64_t a_off = (uint64_t)(((k >> 2) * Cfg::A_CHUNK + (k & 3) * 32) >> 4);
             const uint64_t b_off = (uint64_t)(((k >> 2) * Cfg::B_CHUNK + (k & 3) * 32) >> 4);
-            mma_i8_pair_elect(d_tmem, adesc + a_off, bdesc + b_off, Cfg::IDESC, (k == 0 && first) ? 0u : 1u);
+            mma_i8_pair_elect(d_tmem, adesc + a_off, bdesc + b_off, desc, (k == 0 && first) ? 0u : 1u);
         }
         return;
     }
@@ -619,13 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
-    // work items: the tiles, with SUB those of the partial last round in pieces
-    int ntiles = sh->ntiles, whole = ntiles;
-    if constexpr (Cfg::SUB != 0) {
-        const int rest = ntiles % npairs;
-        whole = ntiles - rest;
-        ntiles = whole + rest * Cfg::PIECES;
-    }
+    const int ntiles = Cfg::SUB ? p.cut_items : sh->ntiles;
     bool aborted_any = false;
 
     if (warp == 0) {
@@ -637,8 +656,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             int s = 0, g_at = 0;
             uint32_t ph = 0;
             for (int t = pair; t < ntiles && !sh->abort; t += npairs) {
-                const TileInfo ti = get_item<Cfg, MODE>(t, whole, rank, p, cum, tiles_n, g_at);
-                const int half_b = (Cfg::SUB ? ti.width : BN) / 2;   // rows of B of this CTA (a box may load more)
+                const TileInfo ti = get_item<Cfg, MODE>(t, rank, p, cum, tiles_n, g_at);
+                const int half_b = (Cfg::SUB ? ti.width : BN) / 2;   // rows of B of this CTA
+                const bool small_b = Cfg::SUB && Cfg::I8 && ti.width < BN;   // (other types load BN / 2 all the same)
                 const int32_t sfa_rt = (int32_t)(ti.row0 / 128);
                 const int32_t sfb_rt = (int32_t)(ti.sfb_rt_base + ti.n0 / 128);
                 const int ktiles = ktiles_of(ti);
@@ -653,14 +673,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                         armed_par = (armed_par & ~(1u << s)) | (ph << s);
                     }
                     if (issuer) {
-                        if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], p.stage_tx);
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(&sh->full[s], p.stage_tx - (small_b ? (BN - Cfg::SUB) * CHUNK * KCH : 0));
 #pragma unroll
                         for (int c = 0; c < KCH; ++c) {
                             const int32_t kx = (int32_t)(ti.k0 / Cfg::KPB) + (kt * KCH + c) * CHUNK;
                             // (dense, one row tile: the odd CTA has no rows of A)
                             if (MODE != MODE_DENSE || rank == 0 || p.M > BM)
                                 tma_load_2d_pair(st + c * Cfg::A_CHUNK, &tma_a, kx, (int32_t)ti.row0, full_leader);
-                            tma_load_2d_pair(st + A_BYTES + c * Cfg::B_CHUNK, &tma_b, kx,
+                            tma_load_2d_pair(st + A_BYTES + c * Cfg::B_CHUNK, small_b ? &tma_z : &tma_b, kx,
                                              (int32_t)(ti.b_row + rank * half_b), full_leader);
                         }
                         // scale atoms: NATOM consecutive K atoms of one (A) or NRT (B) 128-row tiles
@@ -697,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             int acc = 0, g_at = 0;
             uint32_t acc_ph = 0;
             for (int t = pair; t < ntiles && !sh->abort; t += npairs) {
-                const TileInfo ti = get_item<Cfg, MODE>(t, whole, 0, p, cum, tiles_n, g_at);
+                const TileInfo ti = get_item<Cfg, MODE>(t, 0, p, cum, tiles_n, g_at);
                 uint32_t desc = Cfg::IDESC;
                 if constexpr (Cfg::SUB != 0) desc = (desc & ~(63u << 17)) | ((uint32_t)(ti.width >> 3) << 17);
                 const int64_t rt0 = ti.n0 / 128;
@@ -756,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         ring.start(pair, part);
         int g_at = 0;
         for (int t = pair; t < ntiles; t += npairs) {
-            const TileInfo ti = get_item<Cfg, MODE>(t, whole, rank, p, cum, tiles_n, g_at);
+            const TileInfo ti = get_item<Cfg, MODE>(t, rank, p, cum, tiles_n, g_at);
             const int row_lo = 32 * q;
             // int8: this lane's token scale, and the channel scale of column
             // 32 j + lane of the tile, one 32-column step ahead
@@ -770,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 chan = load_chan(0);
             }
             if constexpr (OUT == OUT_GATED_BWD)
-                ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, whole, npairs, rank, row_lo, lane, part);
+                ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
             // one answer for the warp: what follows needs it whole
             if (!__all_sync(0xFFFFFFFFu, wait_phase(&sh->tmem_full[acc], acc_ph, sh, limit))) break;
             tc_fence_after();
@@ -895,7 +916,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     const uint32_t b = ring.used & 1u;
                     uint8_t *buf = ring_bufs + b * EPI_BUF;
                     if (in_ring) {
-                        ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, whole, npairs, rank, row_lo, lane, part);
+                        ring.fill(&tma_z, ring_bufs, ring_bars, p, cum, tiles_n, ntiles, npairs, rank, row_lo, lane, part);
                         // one answer for the warp: the tensor memory instructions need it whole
                         ok = __all_sync(0xFFFFFFFFu, wait_phase(&ring_bars[b], (ring.used >> 1) & 1u, sh, limit));
                         if (ok) unstage_row128(smem_u32(buf), lane, w);
@@ -934,7 +955,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 // 64 columns per step: two 32-column TMEM loads rounded to
                 // bf16 pairs (RNE), one 128-byte row segment per lane
                 const uint32_t tm = tmem + ((uint32_t)(32 * q) << 16) + (acc ? Cfg::ACC1_COL : 0u);
-                for (int j = 0; j < BN / 64; ++j) {
+                const int steps = (Cfg::SUB ? ti.width : BN) / 64;
+                for (int j = 0; j < steps; ++j) {
                     uint32_t w[32];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -956,7 +978,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                         for (int i = 0; i < 16; ++i)
                             w[16 * h + i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                     }
-                    if (j == BN / 64 - 1) {
+                    if (j == steps - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
@@ -999,7 +1021,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     }
                 }
             } else {
-                for (int j = 0; j < BN / 32; ++j) {
+                const int steps = (Cfg::SUB ? ti.width : BN) / 32;
+                for (int j = 0; j < steps; ++j) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + (acc ? Cfg::ACC1_COL : 0u) + 32u * j, v);
                     tmem_ld_wait();
@@ -1013,7 +1036,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     }
                     if constexpr (Cfg::I8) scale_i8(v, tok, chan);
                     if constexpr (Cfg::I8) chan = load_chan(j + 1);
-                    if (j == BN / 32 - 1) {
+                    if (j == steps - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
@@ -1185,6 +1208,7 @@ struct GemmArgs {
     void *z = nullptr;
     int64_t ldz = 0;
     float alpha = 1.0f, limit = 0.0f, beta = 0.0f;
+    int cut_whole = 0, cut_tiles = 0, cut_last = 0, cut_items = 0;
 };
 
 // Returns 0 on success, MXFP4_ERR_CUDA when a map or launch fails.
@@ -1231,6 +1255,10 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     if ((OUT == OUT_GATED || OUT == OUT_GATED_BWD) && g.z &&
         !make_map(&tz, BF, g.z, OUT == OUT_GATED ? N : 2 * N, (uint64_t)c_rows, (uint64_t)g.ldz * 2, 64, 32, SW128))
         return MXFP4_ERR_CUDA;
+    if constexpr (Cfg::I8 && Cfg::SUB)         // B's boxes of a piece
+        if (!make_map(&tz, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b_codes, kbytes, (uint64_t)G * N, (uint64_t)g.ldb, CHUNK,
+                      Cfg::SUB / 2, SW128))
+            return MXFP4_ERR_CUDA;
     // scale atoms as a 3D tensor [128-row tile][K atom][512 bytes = 128 x 32-bit]:
     // one box holds NATOM consecutive atoms of one (A) or NRT (B) row tiles
     if constexpr (!Cfg::I8)
@@ -1250,6 +1278,7 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     p.a_tok = g.a_tok; p.b_chan = g.b_chan;
     p.z = g.z; p.ldz = g.ldz;
     p.act_alpha = g.alpha; p.act_limit = g.limit; p.act_beta = g.beta;
+    p.cut_whole = g.cut_whole; p.cut_tiles = g.cut_tiles; p.cut_last = g.cut_last; p.cut_items = g.cut_items;
     p.wait_limit_ns = g_wait_limit_ns;
     p.stage_tx = Cfg::STAGE_TX - (uint32_t)(Cfg::KCH * (BM - a_box) * CHUNK) -
                  (MODE == MODE_DENSE && g.M <= BM ? (uint32_t)Cfg::A_BYTES : 0u);
@@ -1257,7 +1286,8 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     int pairs = pairs_max;
     if (MODE != MODE_GROUPED_M) {
         const int64_t tiles = (MODE == MODE_GROUPED_K ? g.G : 1) * ((g.M + 255) / 256) * ((g.N + BN - 1) / BN);
-        pairs = (int)(tiles * Cfg::PIECES < pairs_max ? tiles * Cfg::PIECES : pairs_max);
+        const int64_t items = Cfg::SUB ? g.cut_items : tiles;
+        pairs = (int)(items < pairs_max ? items : pairs_max);
     }
     const cudaError_t e = launch_pdl(mxfp4_gemm_kernel<Cfg, MODE, OUT>, dim3((unsigned)(2 * pairs)), dim3(Cfg::THREADS),
                                      (size_t)Cfg::SMEM_BYTES, s, ta, tb, tc, tsa, tsb, tz, p);
@@ -1328,8 +1358,19 @@ template <class Cfg, class Cut, int MODE, int OUT>
 static int launch_cut(const GemmArgs &g, cudaStream_t s) {
     if constexpr (Cut::SUB != 0) {
         static_assert(MODE == MODE_DENSE && Cut::BN == Cfg::BN, "the same tiles, counted on the host");
-        const int64_t pairs = sm_count() / 2, rest = ((g.M + 255) / 256) * ((g.N + Cfg::BN - 1) / Cfg::BN) % pairs;
-        if (rest && rest * Cut::PIECES <= pairs) return launch_cfg<Cut, MODE, OUT>(g, s);
+        const int64_t pairs = sm_count() / 2, tiles_m = (g.M + 255) / 256, tiles_n = (g.N + Cfg::BN - 1) / Cfg::BN;
+        const int64_t rest = tiles_m * tiles_n % pairs;
+        const int64_t last = !Cut::I8 ? 0 : rest < tiles_m ? rest : tiles_m;      // (M is the fast axis)
+        const int64_t tail = (g.N - (tiles_n - 1) * Cfg::BN + Cut::SUB - 1) / Cut::SUB;
+        const int64_t pieces = (rest - last) * Cut::PIECES + last * tail;
+        if (rest && pieces <= pairs) {
+            GemmArgs c = g;
+            c.cut_whole = (int)(tiles_m * tiles_n - rest);
+            c.cut_tiles = (int)(rest - last);
+            c.cut_last = (int)last;
+            c.cut_items = c.cut_whole + (int)pieces;
+            return launch_cfg<Cut, MODE, OUT>(c, s);
+        }
     }
     return launch_cfg<Cfg, MODE, OUT>(g, s);
 }
@@ -1376,8 +1417,8 @@ int launch_int8_gemm(const Int8Args &a, cudaStream_t s) {
     if (a.offsets)
         return a.bf16 ? launch_tiles<I8GroupedCfg, I8GroupedNarrowCfg, MODE_GROUPED_M, OUT_BF16>(g, s)
                       : launch_tiles<I8GroupedCfg, I8GroupedNarrowCfg, MODE_GROUPED_M, OUT_F32>(g, s);
-    return a.bf16 ? launch_tiles<I8Cfg, I8NarrowCfg, MODE_DENSE, OUT_BF16>(g, s)
-                  : launch_tiles<I8Cfg, I8NarrowCfg, MODE_DENSE, OUT_F32>(g, s);
+    return a.bf16 ? launch_tiles<I8Cfg, I8NarrowCfg, MODE_DENSE, OUT_BF16, I8CutCfg>(g, s)
+                  : launch_tiles<I8Cfg, I8NarrowCfg, MODE_DENSE, OUT_F32, I8CutCfg>(g, s);
 }
 
 int get_error(cudaStream_t s) {

@@ -382,6 +382,12 @@ def test_int8_gemm_sums_are_exact(M, N, K):
         assert torch.all(out[M] == 7) and torch.all(out[:, N:] == 7)
 
 
+@pytest.mark.parametrize("M,N,K", [(2048, 2880, 64), (1900, 2850, 272), (4000, 2880, 48), (1024, 5700, 32), (19000, 250, 32)])
+def test_int8_gemm_last_round_in_pieces(M, N, K):
+    """Several rounds of tiles whose last is cut, the last columns in one piece or two."""
+    test_int8_gemm_sums_are_exact(M, N, K)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 96, 2880), (7, 136, 272), (16, 72, 96), (130, 200, 528)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_int8_gemm_scales(M, N, K, dtype):
