@@ -207,7 +207,8 @@ def test_gated_backward(M, I, K, act):
     assert again is z and torch.equal(z, dz)
 
 
-@pytest.mark.parametrize("M,I,K", [(3500, 1344, 64), (3400, 1332, 192), (23000, 100, 64), (4000, 12, 576), (300, 1152, 320)])
+@pytest.mark.parametrize("M,I,K", [(3500, 1344, 64), (3400, 1332, 192), (23000, 100, 64), (4000, 12, 576), (300, 1152, 320),
+                                   (20, 30000, 64), (100, 30000, 320)])
 def test_gated_backward_last_round_in_pieces(M, I, K):
     """Tiles of one or several rounds whose last is cut: both tile widths, pieces
     that end inside their columns and ones past the last column."""
@@ -382,7 +383,8 @@ def test_int8_gemm_sums_are_exact(M, N, K):
         assert torch.all(out[M] == 7) and torch.all(out[:, N:] == 7)
 
 
-@pytest.mark.parametrize("M,N,K", [(2048, 2880, 64), (1900, 2850, 272), (4000, 2880, 48), (1024, 5700, 32), (19000, 250, 32)])
+@pytest.mark.parametrize("M,N,K", [(2048, 2880, 64), (1900, 2850, 272), (4000, 2880, 48), (1024, 5700, 32), (19000, 250, 32),
+                                   (40, 19500, 48), (100, 19500, 272), (200, 19000, 128)])
 def test_int8_gemm_last_round_in_pieces(M, N, K):
     """Several rounds of tiles whose last is cut, the last columns in one piece or two."""
     test_int8_gemm_sums_are_exact(M, N, K)
