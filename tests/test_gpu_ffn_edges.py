@@ -1,0 +1,51 @@
+"""GPU: calls of the expert feed-forward operators at the edges of what they
+document.  Bounds as in test_gpu_ffn, or derived beside the check."""
+import numpy as np
+import pytest
+
+import ffn_testutil as ffn
+import oracle
+import quantize_block_scaled_rht_b200 as mx
+import synth
+import test_gpu_ffn as base
+from mxfp4_testutil import dev_bf16
+from test_gpu_ffn import GEMM_REL, assert_within, f64, no_error, operand
+
+pytestmark = pytest.mark.gpu
+
+NO_LIMIT = dict(alpha=1.702, limit=float("inf"), beta=0.5)
+
+
+# ------------------------------------------------------------------ gated backward: extreme z
+@pytest.mark.parametrize("act", [ffn.SWIGLU, ffn.CLAMPED, NO_LIMIT])
+@pytest.mark.parametrize("M", [3, 150])
+def test_gated_backward_of_gates_near_the_largest_finite_value(M, act):
+    """alpha g may leave FP32's range although g does not.  A gate far below zero
+    passes nothing.  One far above has s = 1 and 1 - s = 0, so dz = dh (u + beta)
+    and dh g (0 beyond the limit)."""
+    I, K = 72, 128
+    ca, sa, da, dsa = operand(M, K, 3, 1e-2)
+    cb, sb, db, dsb = operand(I, K, 4, 0.1)
+    z = np.random.default_rng(5).standard_normal((M, 2 * I)).astype(np.float32)
+    gates = np.array([-3.3e38, -2.9e38, -2.1e38, 2.1e38, 2.9e38, 3.3e38], np.float32)
+    z[:, 0::2] = gates[np.arange(M * I).reshape(M, I) % 6]
+    zb = synth.bf16_bits(z)
+    dz = f64(mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, dev_bf16(zb), K, **act))
+    no_error()
+    dh, s = oracle.gemm(ca, sa, cb, sb, K)
+    z64 = synth.bf16_to_f32(zb).astype(np.float64)
+    below, above = z64[:, 0::2] < 0, z64[:, 0::2] > 0
+    assert np.all(dz[:, 0::2][below] == 0) and np.all(dz[:, 1::2][below] == 0)
+    g, u = np.minimum(z64[:, 0::2], act["limit"]), np.clip(z64[:, 1::2], -act["limit"], act["limit"])
+    if np.isinf(act["limit"]):
+        # s = 1 and the derivative 1 exactly; two FP32 roundings, then bf16's
+        for k, f in ((0, u + act["beta"]), (1, g)):
+            want = dh * f
+            slack = GEMM_REL * s * np.abs(f) + 3 * 2.0 ** -24 * np.abs(want)
+            assert_within(dz[:, k::2][above], want[above],
+                          (ffn.BF16_HALF * (np.abs(want) + slack) + slack + ffn.FLOOR)[above], "dz")
+    else:
+        assert np.all(dz[:, 0::2][above] == 0)
+        want, bound = ffn.gated_backward(dh, np.where(z64 > 1e30, 100.0, np.maximum(z64, -100.0)), **act), \
+            ffn.gated_backward_bound(dh, GEMM_REL * s, np.where(z64 > 1e30, 100.0, np.maximum(z64, -100.0)), **act)
+        assert_within(dz[:, 1::2][above], want[:, 1::2][above], bound[:, 1::2][above], "dz up")
