@@ -473,7 +473,8 @@ MXFP4_API int mxfp4_grouped_gated_gemm(const uint8_t *a_codes, int64_t lda, cons
  *     s = sigmoid(alpha g)
  *     dz[2j]     = dh[j] (u + beta) s (1 + alpha g (1 - s))   where z[2j] <= limit, else 0
  *     dz[2j + 1] = dh[j] g s                                  where |z[2j + 1]| <= limit, else 0
- * dz bf16 [M or a_rows, 2N] (lddz), rounded once; a NaN in z gives NaN.  dz
+ * dz bf16 [M or a_rows, 2N] (lddz), rounded once; a NaN in z[2j] gives NaN in
+ * both, one in z[2j + 1] in dz[2j + 1] and, unless z[2j] > limit, in dz[2j].  dz
  * may be z itself (same pointer and row stride), or other columns of its buffer;
  * any other overlap is refused.
  * The gradients of X and of the gate_up weight follow from dz by

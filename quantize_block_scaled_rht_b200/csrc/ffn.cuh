@@ -91,8 +91,10 @@ struct GatedAct {
             // or 1 - s; dh g s is du itself
             const float2 hs = mul2(d, s[i]), du = mul2(hs, g[i]);
             const float2 dg = mul2(fma2(a, mul2(du, sub2(one, s[i])), hs), add2(u, b));
-            z[2 * i] = pack_bf16x2(bf16lo(z0) > limit ? 0.0f : dg.x, fabsf(bf16hi(z0)) > limit ? 0.0f : du.x);
-            z[2 * i + 1] = pack_bf16x2(bf16lo(z1) > limit ? 0.0f : dg.y, fabsf(bf16hi(z1)) > limit ? 0.0f : du.y);
+            // beyond the limit 0, and NaN where zu is
+            const float2 o = sub2(u, u);
+            z[2 * i] = pack_bf16x2(bf16lo(z0) > limit ? 0.0f : dg.x, fabsf(bf16hi(z0)) <= limit ? du.x : o.x);
+            z[2 * i + 1] = pack_bf16x2(bf16lo(z1) > limit ? 0.0f : dg.y, fabsf(bf16hi(z1)) <= limit ? du.y : o.y);
         }
     }
 };

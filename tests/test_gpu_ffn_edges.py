@@ -49,3 +49,28 @@ def test_gated_backward_of_gates_near_the_largest_finite_value(M, act):
         want, bound = ffn.gated_backward(dh, np.where(z64 > 1e30, 100.0, np.maximum(z64, -100.0)), **act), \
             ffn.gated_backward_bound(dh, GEMM_REL * s, np.where(z64 > 1e30, 100.0, np.maximum(z64, -100.0)), **act)
         assert_within(dz[:, 1::2][above], want[:, 1::2][above], bound[:, 1::2][above], "dz up")
+
+
+@pytest.mark.parametrize("act", [ffn.SWIGLU, ffn.CLAMPED])
+@pytest.mark.parametrize("M", [3, 150])
+def test_gated_backward_nan_pre_activations(M, act):
+    """NaN in a gate gives NaN in both gradients of the pair, NaN in an up value in
+    its own and, unless the gate is beyond the limit, in the gate's."""
+    I, K = 72, 128
+    _, _, da, dsa = operand(M, K, 3, 1e-2)
+    _, _, db, dsb = operand(I, K, 4, 0.1)
+    z = dev_bf16(synth.normal_bf16((M, 2 * I), 5, 1.0))
+    clean = f64(mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, z, K, **act))
+    z[1, 10] = float("nan")                # gate of pair 5
+    z[2, 21] = float("nan")                # up of pair 10
+    z[0, 30], z[0, 31] = 8.0, float("nan")
+    dz = f64(mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, z, K, **act))
+    no_error()
+    bad = np.zeros(dz.shape, bool)
+    bad[1, 10:12] = bad[2, 20:22] = True
+    bad[0, 31], bad[0, 30] = True, np.isinf(act["limit"])
+    assert np.array_equal(np.isnan(dz), bad)
+    if not np.isinf(act["limit"]):
+        assert dz[0, 30] == 0
+    bad[0, 30:32] = True
+    assert np.array_equal(dz[~bad], clean[~bad])
