@@ -451,8 +451,9 @@ MXFP4_API int mxfp4_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_
  * once; its sums differ from the tile kernel's in their last bits.
  *
  * Requirements: as mxfp4_gemm / mxfp4_grouped_gemm; N even; h and z 16-byte
- * aligned, ldh % 8 == 0, ldz % 8 == 0, sharing no element; alpha and beta finite,
- * limit > 0.
+ * aligned, ldh % 8 == 0, ldz % 8 == 0, sharing no element with each other or an
+ * operand (other columns of an operand's buffer, at its row stride, are apart);
+ * alpha and beta finite, limit > 0.
  */
 MXFP4_API int mxfp4_gated_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales,
                                const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales,
@@ -476,7 +477,7 @@ MXFP4_API int mxfp4_grouped_gated_gemm(const uint8_t *a_codes, int64_t lda, cons
  * dz bf16 [M or a_rows, 2N] (lddz), rounded once; a NaN in z[2j] gives NaN in
  * both, one in z[2j + 1] in dz[2j + 1] and, unless z[2j] > limit, in dz[2j].  dz
  * may be z itself (same pointer and row stride), or other columns of its buffer;
- * any other overlap is refused.
+ * any other overlap, and dz over an operand, is refused.
  * The gradients of X and of the gate_up weight follow from dz by
  * mxfp4_quantize_dual and the products of mxfp4_gemm and
  * mxfp4_grouped_gemm_wgrad.  Requirements as for the forward form (N need not
@@ -501,7 +502,7 @@ MXFP4_API int mxfp4_grouped_gated_gemm_backward(const uint8_t *a_codes, int64_t 
  * The value of a code is code * scale.  A NaN or Inf in a row gives it the
  * scale NaN and codes 0.  codes [rows, cols] (ld_codes bytes), scales [rows].
  * Requirements: rows, cols > 0; cols % 16 == 0; x and codes 16-byte aligned,
- * ld_x % 8 == 0, ld_codes % 16 == 0.
+ * ld_x % 8 == 0, ld_codes % 16 == 0; x, codes and scales share no byte.
  */
 MXFP4_API int mxfp4_int8_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int8_t *codes,
                                   int64_t ld_codes, float *scales, void *stream);
@@ -521,7 +522,7 @@ MXFP4_API int mxfp4_int8_quantize(const void *x, int64_t rows, int64_t cols, int
  *
  * Requirements: M, N >= 1; K >= 16, K % 16 == 0, K < 131072 (no sum leaves 32
  * bits); codes and c 16-byte aligned; lda, ldb % 16 == 0; ldc * element size %
- * 16 == 0.
+ * 16 == 0; c shares no byte with an operand.
  */
 MXFP4_API int mxfp4_int8_gemm(const int8_t *a_codes, int64_t lda, const float *a_scales,
                               const int8_t *b_codes, int64_t ldb, const float *b_scales,

@@ -3,6 +3,7 @@
 // memory is allocated here; errors come back as status codes.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
@@ -432,15 +433,33 @@ static bool valid_act(float alpha, float limit, float beta) {
     return std::isfinite(alpha) && limit > 0.0f && std::isfinite(beta);   // limit may be infinite
 }
 
-// Whether two row-major arrays of `rows` rows (row strides and widths in bytes)
-// share no byte: apart in memory, or different columns of one buffer.
-static bool disjoint(const void *p, int64_t ld_p, int64_t w_p, const void *q, int64_t ld_q, int64_t w_q, int64_t rows) {
-    const char *p0 = static_cast<const char *>(p), *q0 = static_cast<const char *>(q);
-    const char *p1 = p0 + (rows - 1) * ld_p + w_p, *q1 = q0 + (rows - 1) * ld_q + w_q;
-    if (p1 <= q0 || q1 <= p0) return true;
-    if (ld_p != ld_q) return false;
-    const int64_t d = ((q0 - p0) % ld_p + ld_p) % ld_p;      // column of q in p's rows
-    return w_p <= d && d + w_q <= ld_p;
+// A row-major array in memory: row stride and width in bytes.
+struct Array {
+    const void *p;
+    int64_t ld, width, rows;
+};
+static Array flat(const void *p, int64_t bytes) { return {p, bytes, bytes, 1}; }
+static Array mma_scales(const void *p, int64_t rows, int64_t K, int64_t operands = 1) {
+    return flat(p, operands * mxfp4_mma_scales_bytes(rows, K));
+}
+
+// Whether two arrays share no byte: apart in memory, or different columns of one
+// buffer.
+static bool disjoint(const Array &a, const Array &b) {
+    const char *a0 = static_cast<const char *>(a.p), *b0 = static_cast<const char *>(b.p);
+    const char *a1 = a0 + (a.rows - 1) * a.ld + a.width, *b1 = b0 + (b.rows - 1) * b.ld + b.width;
+    if (a1 <= b0 || b1 <= a0) return true;
+    if (a.ld != b.ld) return false;
+    const int64_t d = ((b0 - a0) % a.ld + a.ld) % a.ld;      // column of b in a's rows
+    return a.width <= d && d + b.width <= a.ld;
+}
+
+// Whether an output shares no byte with any operand (a null one stands for none).
+static bool clear_of(const Array &out, std::initializer_list<Array> operands) {
+    if (!out.p) return true;
+    for (const Array &o : operands)
+        if (o.p && !disjoint(out, o)) return false;
+    return true;
 }
 
 // Row-major bf16 [rows, cols]: 16-byte rows.
@@ -467,10 +486,14 @@ static int gated_impl(const mxfp4::GatedArgs &a, void *stream) {
         if (rc != MXFP4_OK) return rc;
     }
     // z and the output: apart, or (backward) the same buffer with the same rows
-    if (a.z && !(a.backward && a.z == a.out && a.ldz == a.ld_out) &&
-        !disjoint(a.z, 2 * a.ldz, 2 * zcols, a.out, 2 * a.ld_out, a.backward ? 4 * a.N : a.N, a.M))
-        return MXFP4_ERR_INVALID_ARG;
+    const Array out{a.out, 2 * a.ld_out, a.backward ? 4 * a.N : a.N, a.M}, z{a.z, 2 * a.ldz, 2 * zcols, a.M};
+    if (a.z && !(a.backward && a.z == a.out && a.ldz == a.ld_out) && !disjoint(z, out)) return MXFP4_ERR_INVALID_ARG;
     if (a.M > (int64_t)1 << 31 || a.N > (int64_t)1 << 30) return MXFP4_ERR_UNSUPPORTED;
+    const std::initializer_list<Array> operands = {
+        {a.a_codes, a.lda, a.K / 2, a.M},      {a.b_codes, a.ldb, a.K / 2, a.G * a.N},
+        mma_scales(a.a_scales, a.M, a.K),      mma_scales(a.b_scales, a.N, a.K, a.G),
+        flat(a.offsets, 4 * (a.G + 1)),        flat(a.sizes, 4 * a.G)};
+    if (!clear_of(out, operands) || (!a.backward && !clear_of(z, operands))) return MXFP4_ERR_INVALID_ARG;
     return mxfp4::launch_gated(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -531,6 +554,8 @@ int mxfp4_int8_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld_x,
         (reinterpret_cast<uintptr_t>(scales) & 3u))
         return MXFP4_ERR_ALIGNMENT;
     if (rows >= (int64_t)1 << 31) return MXFP4_ERR_UNSUPPORTED;
+    const Array in{x, 2 * ld_x, 2 * cols, rows}, out{codes, ld_codes, cols, rows}, sc = flat(scales, 4 * rows);
+    if (!disjoint(in, out) || !disjoint(in, sc) || !disjoint(out, sc)) return MXFP4_ERR_INVALID_ARG;
     const cudaError_t e = mxfp4::launch_int8_quantize(x, rows, cols, ld_x, codes, ld_codes, scales,
                                                       static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
@@ -547,6 +572,12 @@ static int int8_gemm_impl(const mxfp4::Int8Args &a, int out_dtype, void *stream)
         return MXFP4_ERR_ALIGNMENT;
     // sums of K products up to 2^14 must stay below 2^31
     if (a.K >= 131072 || a.M > (int64_t)1 << 31 || a.N > (int64_t)1 << 31) return MXFP4_ERR_UNSUPPORTED;
+    const int64_t size = a.bf16 ? 2 : 4;
+    const std::initializer_list<Array> operands = {
+        {a.a, a.lda, a.K, a.M},                {a.b, a.ldb, a.K, a.G * a.N},
+        flat(a.a_scales, 4 * a.M),             flat(a.b_scales, 4 * a.G * a.N),
+        flat(a.offsets, 4 * (a.G + 1)),        flat(a.sizes, 4 * a.G)};
+    if (!clear_of({a.c, size * a.ldc, size * a.N, a.M}, operands)) return MXFP4_ERR_INVALID_ARG;
     return mxfp4::launch_int8_gemm(a, static_cast<cudaStream_t>(stream));
 }
 
@@ -583,9 +614,9 @@ int mxfp4_dropout(const void *x, int64_t ld_x, const void *residual, int64_t ld_
         return MXFP4_ERR_ALIGNMENT;
     // in place element for element (y over x or over the residual), or apart
     const int64_t sz = (int64_t)size, w = sz * cols;
+    auto array = [&](const void *q, int64_t ld) { return Array{q, rows == 1 ? w : sz * ld, w, rows}; };
     auto bad = [&](const void *q, int64_t ld) {
-        return q && !(q == y && (rows == 1 || ld == ld_y)) &&
-               !disjoint(q, rows == 1 ? w : sz * ld, w, y, rows == 1 ? w : sz * ld_y, w, rows);
+        return q && !(q == y && (rows == 1 || ld == ld_y)) && !disjoint(array(q, ld), array(y, ld_y));
     };
     if (bad(x, ld_x) || bad(residual, ld_residual)) return MXFP4_ERR_INVALID_ARG;
     const cudaError_t e = mxfp4::launch_dropout(x, ld_x, residual, ld_residual, rows, cols, dtype, p, seed, elem_offset,

@@ -2,6 +2,7 @@
 document.  Bounds as in test_gpu_ffn, or derived beside the check."""
 import numpy as np
 import pytest
+import torch
 
 import ffn_testutil as ffn
 import oracle
@@ -74,3 +75,31 @@ def test_gated_backward_nan_pre_activations(M, act):
         assert dz[0, 30] == 0
     bad[0, 30:32] = True
     assert np.array_equal(dz[~bad], clean[~bad])
+
+
+# ------------------------------------------------------------------ one buffer
+def test_outputs_in_other_columns_of_an_operands_buffer():
+    """Refused only where bytes are shared: h, z, the int8 product and its codes beside
+    the operand they come from, at its row stride."""
+    M, I, K = 150, 64, 128
+    _, _, da, dsa = operand(M, K, 1, 1.0)
+    _, _, db, dsb = operand(2 * I, K, 2, 0.2)
+    want = mx.mxfp4_gated_gemm(da, dsa, db, dsb, K, save_z=True)
+    buf = torch.zeros((M, K // 2 + 6 * I), dtype=torch.uint8, device="cuda")
+    buf[:, :K // 2] = da
+    wide = buf.view(torch.bfloat16)
+    h, z = wide[:, K // 4:K // 4 + I], wide[:, K // 4 + I:]
+    mx.mxfp4_gated_gemm(buf[:, :K // 2], dsa, db, dsb, K, out=h, z_out=z)
+    assert torch.equal(h, want[0]) and torch.equal(z, want[1]) and torch.equal(buf[:, :K // 2], da)
+    want = mx.mxfp4_int8_quantize(want[0])
+    buf = torch.zeros((M, 4 * I), dtype=torch.int8, device="cuda")
+    x = buf.view(torch.bfloat16)[:, :I]
+    x.copy_(h)
+    q = mx.mxfp4_int8_quantize(x, out=mx.Int8Quantized(buf[:, 2 * I:3 * I], torch.empty(M, device="cuda")))
+    assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales) and torch.equal(x, h)
+    one = torch.ones(M, device="cuda")
+    y = mx.mxfp4_int8_gemm(want.codes, one, want.codes[:I // 4], one[:I // 4])
+    out = buf.view(torch.bfloat16)[:, 3 * I // 2:3 * I // 2 + I // 4]
+    mx.mxfp4_int8_gemm(q.codes, one, want.codes[:I // 4], one[:I // 4], out=out)
+    assert torch.equal(out, y) and torch.equal(q.codes, want.codes)
+    no_error()
