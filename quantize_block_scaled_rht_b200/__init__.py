@@ -551,8 +551,11 @@ def mxfp4_scales_to_mma(scales: torch.Tensor, rows: int, k: int, two_d: bool = F
 
 # Host time counts where one token's kernels take a few microseconds, so the
 # common path (tensors on the current device, its current stream) does nothing
-# twice and looks nothing up twice.
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# twice and looks nothing up twice.  A torch without these two names (a build for
+# the CPU, or another version) gives the public functions, so that what needs no
+# device still imports and runs.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda idx: torch.cuda.current_stream(idx).cuda_stream)
 _U8, _I8, _BF16, _F32 = torch.uint8, torch.int8, torch.bfloat16, torch.float32
 
 
