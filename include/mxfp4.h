@@ -97,7 +97,9 @@ MXFP4_API const char *mxfp4_status_string(int status);
  * mxfp4_grouped_gemm_wgrad_bf16; 1.04 mxfp4_scales_to_mma; 1.05
  * mxfp4_quantize_dual_rows.  The expert feed-forward entry points
  * (mxfp4_gated_*, mxfp4_int8_*, mxfp4_dropout) came after 1.05 and leave it
- * unchanged: they add symbols and change none. */
+ * unchanged: they add symbols and change none.  A caller tells a header that has
+ * them by MXFP4_HAS_FFN, and a library by looking one of them up (dlsym). */
+#define MXFP4_HAS_FFN 1
 MXFP4_API int mxfp4_version(void);
 
 /*

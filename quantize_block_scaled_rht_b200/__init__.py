@@ -67,6 +67,10 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"libmxfp4.so not built: run `python -m quantize_block_scaled_rht_b200.build` ({LIB_PATH})")
         L = ctypes.CDLL(LIB_PATH)
+        missing = [f for f in ABI_FUNCTIONS if not hasattr(L, f)]
+        if missing:     # the version alone does not tell: it stands for what 1.05 had
+            raise ImportError(f"{LIB_PATH} was built from older sources (no {', '.join(missing)}): run "
+                              f"`python -m quantize_block_scaled_rht_b200.build --force`")
         i64, u64, i32, vp = ctypes.c_int64, ctypes.c_uint64, ctypes.c_int, ctypes.c_void_p
         L.mxfp4_status_string.argtypes = [i32]
         L.mxfp4_status_string.restype = ctypes.c_char_p

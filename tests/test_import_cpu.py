@@ -38,13 +38,36 @@ assert torch.equal(q.codes, r.codes) and int(q.codes.abs().max()) == 127
 """
 
 
-def _python(code):
-    r = subprocess.run([sys.executable, "-c", code, ROOT], capture_output=True, text=True, timeout=600)
+def _python(code, *args):
+    r = subprocess.run([sys.executable, "-c", code, ROOT, *args], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_import_without_the_cuda_names_of_torch():
     _python(IMPORT)
+
+
+OLD_LIBRARY = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import quantize_block_scaled_rht_b200 as mx
+mx.LIB_PATH = sys.argv[2]
+try:
+    mx.mma_scales_bytes(128, 128)
+except ImportError as e:
+    assert "older sources" in str(e) and "mxfp4_dropout" in str(e) and "mxfp4_version" not in str(e), e
+else:
+    raise SystemExit("taken")
+"""
+
+
+def test_a_library_without_the_newer_symbols_is_named(tmp_path):
+    """A library of the same version number that lacks entry points is refused when
+    it is loaded, with their names."""
+    src, so = tmp_path / "old.c", tmp_path / "libold.so"
+    src.write_text("int mxfp4_version(void) { return 105; }\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
+    _python(OLD_LIBRARY, str(so))
 
 
 @pytest.mark.gpu
