@@ -455,7 +455,7 @@ MXFP4_API int mxfp4_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_
  * Requirements: as mxfp4_gemm / mxfp4_grouped_gemm; N even; h and z 16-byte
  * aligned, ldh % 8 == 0, ldz % 8 == 0, sharing no element with each other or an
  * operand (other columns of an operand's buffer, at its row stride, are apart);
- * alpha and beta finite, limit > 0.
+ * |alpha| < 2.3e38, beta finite, limit > 0.
  */
 MXFP4_API int mxfp4_gated_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales,
                                const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales,

@@ -430,7 +430,8 @@ int mxfp4_scales_to_mma(const uint8_t *scales, int64_t ld_scales, int64_t rows, 
 
 // Gated forms: the activation's numbers, then the bf16 output(s).
 static bool valid_act(float alpha, float limit, float beta) {
-    return std::isfinite(alpha) && limit > 0.0f && std::isfinite(beta);   // limit may be infinite
+    // limit may be infinite; alpha goes into the exponent times log2(e)
+    return std::isfinite(alpha * 1.44269504f) && limit > 0.0f && std::isfinite(beta);
 }
 
 // A row-major array in memory: row stride and width in bytes.

@@ -101,3 +101,12 @@ def test_int8_quantizer_over_its_input():
         assert quantize(OUT, scales) == BAD
     for scales in (OUT, OUT + 64 * M - 4, OUT - 4 * M + 4):
         assert quantize(OUT, scales) == BAD
+
+
+@pytest.mark.parametrize("alpha", [3e38, -3e38, 2.4e38])
+def test_alpha_whose_exponent_factor_overflows(alpha):
+    """alpha * log2(e) has to be finite: times a gate of 0 an infinity would give NaN."""
+    L = mx.lib()
+    assert L.mxfp4_gated_gemm(at(A), 32, at(SA), at(B), 32, at(SB), M, N, K, alpha, INF, 0.0, at(OUT), 64, None, 0, None) == BAD
+    assert L.mxfp4_gated_gemm_backward(at(A), 32, at(SA), at(B), 32, at(SB), M, N, K, alpha, INF, 0.0, at(Z), 256, at(OUT), 256,
+                                       None) == BAD
