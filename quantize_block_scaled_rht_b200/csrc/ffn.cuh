@@ -123,13 +123,25 @@ struct Int8Args {
     int G;
 };
 
-// Products of few rows (rows.cu): at most ROWS_MAX, handled 1, 2 or 4 at a
-// time; the gated one also needs that many rows of A, one byte per element and
-// scale, in 48 KB of shared memory (less what the kernel has besides).
+// Products of few rows (rows.cu): at most ROWS_MAX, handled 1, 2 or 4 at a time.
+// Their integer work goes with rows * N * K, while the tile kernel's time goes
+// with K (a first round of tiles: about (5000 + K) * 0.9 ns) until N fills the
+// device, and hardly with the rows.  The limits are where the two times meet (41
+// sizes, N 256 to 178560, K 256 to 8192, weights in L2 and from HBM): by these
+// rules no size is more than 6% (gated) or 5% (int8) off the faster kernel, where
+// all calls of up to four rows by the streaming kernel were up to 2.9 and 1.7
+// times slower (4 rows of 178560 x 2880: gated 199 us against 68, int8 156
+// against 94).  One int8 row streams B as fast as the tile kernel at any size
+// (178560 x 2880: 91 us, 94 there).
 constexpr int64_t ROWS_MAX = 4;
 inline int64_t rows_handled(int64_t M) { return M <= 2 ? M : 4; }
-inline bool gated_rows_fit(int64_t M, int64_t K) {
-    return M <= ROWS_MAX && rows_handled(M) * (K + K / 32) <= 47 * 1024;
+// The gated kernel also needs the rows of A, one byte per element and scale, in 48
+// KB of shared memory (less what it has besides).
+inline bool gated_by_rows(int64_t M, int64_t N, int64_t K) {
+    return M <= ROWS_MAX && rows_handled(M) * (K + K / 32) <= 47 * 1024 && rows_handled(M) * N * K <= 5700 * (5000 + K);
+}
+inline bool int8_by_rows(int64_t M, int64_t N, int64_t K) {
+    return M <= ROWS_MAX && (rows_handled(M) - 1) * N * K <= 25000 * (5000 + K);
 }
 int launch_gated_rows(const GatedArgs &a, cudaStream_t s);
 int launch_int8_rows(const Int8Args &a, cudaStream_t s);

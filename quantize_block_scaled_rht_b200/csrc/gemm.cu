@@ -1393,7 +1393,7 @@ static int launch_tiles(const GemmArgs &g, cudaStream_t s) {
 // Gated products: the activation of column pairs of A B^T (forward), or dz from
 // dh = A B^T and z (backward); offsets null for the dense forms.
 int launch_gated(const GatedArgs &a, cudaStream_t s) {
-    if (!a.offsets && !a.backward && gated_rows_fit(a.M, a.K)) return launch_gated_rows(a, s);
+    if (!a.offsets && !a.backward && gated_by_rows(a.M, a.N, a.K)) return launch_gated_rows(a, s);
     GemmArgs g{a.a_codes, a.a_scales, a.b_codes, a.b_scales, a.lda, a.ldb, a.M, a.N, a.K, a.ld_out, a.out, a.offsets,
                a.sizes, a.offsets ? a.G : 1};
     g.z = a.z;
@@ -1409,7 +1409,7 @@ int launch_gated(const GatedArgs &a, cudaStream_t s) {
 }
 
 int launch_int8_gemm(const Int8Args &a, cudaStream_t s) {
-    if (!a.offsets && a.M <= ROWS_MAX) return launch_int8_rows(a, s);
+    if (!a.offsets && int8_by_rows(a.M, a.N, a.K)) return launch_int8_rows(a, s);
     GemmArgs g{reinterpret_cast<const uint8_t *>(a.a), nullptr, reinterpret_cast<const uint8_t *>(a.b), nullptr, a.lda,
                a.ldb, a.M, a.N, a.K, a.ldc, a.c, a.offsets, a.sizes, a.offsets ? a.G : 1};
     g.a_tok = a.a_scales;

@@ -2,13 +2,16 @@
 // four tokens of decoding), where the time is reading B once.
 //
 // A tile of the tensor-core kernel would be almost empty there, and its 30 to 45
-// tiles would leave most SMs without a load in flight: gated 5760 x 2880, 1 / 4
-// rows 5.0 / 7.9 us against 8.3 there, int8 2880 x 2880 2.5 / 4.0 against 11.4
-// (weights in L2).  The integer work grows with the rows: at 8 rows 11.6 and 7.0
-// us, and 23 against 13 on gated 5760 x 5760, so the tile kernel takes over at 5.  Here a CTA takes 8 rows
-// of B: two groups of four rows, each walked by four warps that take the steps
-// of K in turn, eight lanes to a row with 16 bytes each (128 consecutive bytes
-// of a row per step).  Products are integer: four at a time by dp4a, an E2M1
+// tiles would leave most SMs without a load in flight: 5760 x 2880, 1 / 2 / 4 rows,
+// gated 5.0 / 6.3 / 8.1 us against 7.4 there, int8 3.9 / 4.2 / 5.1 against 9.9
+// (weights in L2; from HBM 5.7 / 6.8 / 9.8 against 8.0, and 5.5 / 6.0 / 6.8 against
+// 11.0).  The integer work grows with the rows, so the tile kernel takes over where
+// rows * N * K outgrows it (gated_by_rows, int8_by_rows), and at 5 rows: an
+// 8-row gated form takes 11.8 us at that size, and an int8 one 12.3 (and 11.5
+// against 14.5 at 2880 x 5760, 4.8 against 7.2 at 2880 x 1472: it was not kept).
+// Here a CTA takes 8 rows of B: two groups of four rows, each walked by four
+// warps that take the steps of K in turn, eight lanes to a row with 16 bytes each
+// (128 consecutive bytes of a row per step).  Products are integer: four at a time by dp4a, an E2M1
 // value doubled to one of 0, +-1, +-2, +-3, +-4, +-6, +-8, +-12.
 #include <cstdint>
 

@@ -103,3 +103,25 @@ def test_outputs_in_other_columns_of_an_operands_buffer():
     mx.mxfp4_int8_gemm(q.codes, one, want.codes[:I // 4], one[:I // 4], out=out)
     assert torch.equal(out, y) and torch.equal(q.codes, want.codes)
     no_error()
+
+
+# ------------------------------------------------------------------ few rows, large products
+@pytest.mark.parametrize("M,I,K", [(1, 226_000, 64), (2, 3300, 4096), (3, 2900, 2880), (4, 2900, 2880), (3, 56_600, 64),
+                                   (4, 1500, 2880), (2, 2200, 4096)])
+@pytest.mark.parametrize("keep", [False, True])
+def test_gated_few_rows_on_both_sides_of_the_kernels_limit(M, I, K, keep):
+    """One to four rows by the tile kernel and (the last two sizes) the streaming one."""
+    base.test_gated_gemm(M, I, K, keep, ffn.CLAMPED)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 2_000_000, 64), (3, 209_000, 208), (4, 209_000, 208), (1, 500_000, 208),
+                                   (4, 60_000, 208)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_int8_few_rows_on_both_sides_of_the_kernels_limit(M, N, K, dtype):
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    a = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    b = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    out = mx.mxfp4_int8_gemm(a, torch.ones(M, device="cuda"), b, torch.ones(N, device="cuda"), out_dtype=dtype)
+    no_error()
+    # unit scales and sums below 2^24: exact in FP32, bf16 the sum rounded once
+    assert torch.equal(out, (a.double() @ b.double().t()).to(torch.float32).to(dtype))
