@@ -125,3 +125,122 @@ def test_int8_few_rows_on_both_sides_of_the_kernels_limit(M, N, K, dtype):
     no_error()
     # unit scales and sums below 2^24: exact in FP32, bf16 the sum rounded once
     assert torch.equal(out, (a.double() @ b.double().t()).to(torch.float32).to(dtype))
+
+
+# ------------------------------------------------------------------ columns that end inside 16 bytes
+def padded(t):
+    """t as the first columns of rows that start on 16 bytes, as the operators take them."""
+    rows, cols = t.shape
+    wide = torch.full((rows, (cols + 15) // 8 * 8), 11.0, dtype=t.dtype, device="cuda")
+    wide[:, :cols] = t
+    return wide[:, :cols]
+
+
+def check_backward(M, I, K, act):
+    ca, sa, da, dsa = operand(M, K, M + 1, 1e-2)
+    cb, sb, db, dsb = operand(I, K, I + 1, 1.0 / K ** 0.5)
+    zb = base.z_values(M, I, M + I)
+    z = padded(dev_bf16(zb))
+    dz = mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, z, K, **act)
+    no_error()
+    dh, s = oracle.gemm(ca, sa, cb, sb, K)
+    z64 = synth.bf16_to_f32(zb).astype(np.float64)
+    assert dz.shape == (M, 2 * I)
+    assert_within(f64(dz), ffn.gated_backward(dh, z64, **act), ffn.gated_backward_bound(dh, GEMM_REL * s, z64, **act), "dz")
+    mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, z, K, **act, out=z)       # in place
+    assert torch.equal(z, dz) and torch.all(z._base[:, 2 * I:] == 11)
+
+
+ODD = [(1, 1, 64), (3, 7, 128), (5, 33, 64), (40, 2, 64), (130, 101, 320), (128, 98, 512), (300, 31, 2880), (257, 501, 576),
+       (64, 1606, 64), (1000, 263, 192), (1300, 2182, 128)]
+
+
+@pytest.mark.parametrize("act", base.ACTS)
+@pytest.mark.parametrize("M,I,K", ODD)
+def test_gated_odd_columns(M, I, K, act):
+    ca, sa, da, dsa = operand(M, K, M + K, 1.5)
+    cb, sb, db, dsb = operand(2 * I, K, I, 2.0 / K ** 0.5)
+    h, z = mx.mxfp4_gated_gemm(da, dsa, db, dsb, K, **act, save_z=True)
+    no_error()
+    ref, s = oracle.gemm(ca, sa, cb, sb, K)
+    assert h.shape == (M, I) and z.shape == (M, 2 * I)
+    assert_within(f64(h), ffn.gated(ref, **act), ffn.gated_bound(ref, GEMM_REL * s, **act), "h")
+    assert_within(f64(z), ref, ffn.BF16_HALF * (np.abs(ref) + GEMM_REL * s) + GEMM_REL * s + ffn.FLOOR, "z")
+    check_backward(M, I, K, act)
+
+
+@pytest.mark.parametrize("M,I,K", [(3500, 1343, 64), (23000, 99, 64), (4000, 13, 576), (20, 29998, 64), (100, 29999, 320)])
+def test_gated_backward_odd_columns_last_round_in_pieces(M, I, K):
+    check_backward(M, I, K, ffn.CLAMPED)
+
+
+@pytest.mark.parametrize("I", [55, 57, 58])
+@pytest.mark.parametrize("M", [4, 150])
+def test_gated_odd_columns_leave_what_stands_behind_them(M, I):
+    K = 128
+    ca, sa, da, dsa = operand(M, K, 41, 1e-2)
+    cb, sb, db, dsb = operand(I, K, 42, 0.1)
+    zb = base.z_values(M, I, 43)
+    ldz = (2 * I + 37) // 8 * 8
+    z = torch.full((M + 1, ldz), 11.0, dtype=torch.bfloat16, device="cuda")
+    z[:M, :2 * I] = dev_bf16(zb)
+    out = torch.full((M + 1, ldz + 8), 13.0, dtype=torch.bfloat16, device="cuda")
+    mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, z[:M, :2 * I], K, **ffn.CLAMPED, out=out[:M, :2 * I])
+    no_error()
+    dh, s = oracle.gemm(ca, sa, cb, sb, K)
+    z64 = synth.bf16_to_f32(zb).astype(np.float64)
+    assert_within(f64(out[:M, :2 * I]), ffn.gated_backward(dh, z64, **ffn.CLAMPED),
+                  ffn.gated_backward_bound(dh, GEMM_REL * s, z64, **ffn.CLAMPED), "dz")
+    assert torch.all(out[:, 2 * I:] == 13) and torch.all(out[M] == 13)
+    mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, z[:M, :2 * I], K, **ffn.CLAMPED, out=z[:M, :2 * I])
+    assert torch.equal(z[:M, :2 * I], out[:M, :2 * I])
+    assert torch.all(z[:, 2 * I:] == 11) and torch.all(z[M] == 11)
+    # forward: h and z in wider buffers
+    _, _, dw, dsw = operand(2 * I, K, 44, 0.1)
+    want_h, want_z = mx.mxfp4_gated_gemm(da, dsa, dw, dsw, K, **ffn.CLAMPED, save_z=True)
+    h = torch.full((M + 1, ldz), 7.0, dtype=torch.bfloat16, device="cuda")
+    zo = torch.full((M + 1, ldz), 9.0, dtype=torch.bfloat16, device="cuda")
+    mx.mxfp4_gated_gemm(da, dsa, dw, dsw, K, **ffn.CLAMPED, out=h[:M, :I], z_out=zo[:M, :2 * I])
+    assert torch.equal(h[:M, :I], want_h) and torch.equal(zo[:M, :2 * I], want_z)
+    assert torch.all(h[:, I:] == 7) and torch.all(h[M] == 7) and torch.all(zo[:, 2 * I:] == 9) and torch.all(zo[M] == 9)
+
+
+@pytest.mark.parametrize("sizes,I,K", [([1, 130, 0, 257, 128], 95, 256), ([300, 5, 64], 202, 576), ([0, 17], 1, 64),
+                                       ([33] * 40, 54, 128), ([700, 900, 0, 100], 2879, 64)])
+def test_grouped_gated_odd_columns(sizes, I, K):
+    """Rows of 2I columns in a wider buffer; the columns behind them and the rows
+    between the groups stay, in place too."""
+    act = ffn.CLAMPED
+    c = base.grouped_operands(sizes, I, K, 51, 1e-2, 0.1, slack=1)
+    w = base.grouped_operands(sizes, 2 * I, K, 61, 1.0, 0.2, slack=1)
+    ld = (2 * I + 15) // 8 * 8
+    z = torch.full((c["rows"], ld), 5.0, dtype=torch.bfloat16, device="cuda")
+    zb = base.z_values(c["rows"], I, 52)
+    z[:, :2 * I] = dev_bf16(zb)
+    out = torch.full((c["rows"], ld), 9.0, dtype=torch.bfloat16, device="cuda")
+    args = (c["a"][2], c["a"][3], c["d_off"], c["d_sizes"], c["b"], c["sb"], z[:, :2 * I], K)
+    mx.mxfp4_grouped_gated_gemm_backward(*args, **act, out=out[:, :2 * I])
+    h = torch.full((w["rows"], ld), 9.0, dtype=torch.bfloat16, device="cuda")
+    zo = torch.full((w["rows"], ld), 9.0, dtype=torch.bfloat16, device="cuda")
+    mx.mxfp4_grouped_gated_gemm(w["a"][2], w["a"][3], w["d_off"], w["d_sizes"], w["b"], w["sb"], K, **act, out=h[:, :I],
+                                z_out=zo[:, :2 * I])
+    no_error()
+    z64 = synth.bf16_to_f32(zb).astype(np.float64)
+    written = torch.zeros(c["rows"], dtype=torch.bool)
+    for g, n in enumerate(sizes):
+        o = int(c["offsets"][g])
+        written[o:o + n] = True
+        if n:
+            dh, s = oracle.gemm(c["a"][0][o:o + n], c["a"][1][o:o + n], c["ws"][g][0], c["ws"][g][1], K)
+            zz = z64[o:o + n]
+            assert_within(f64(out[o:o + n, :2 * I]), ffn.gated_backward(dh, zz, **act),
+                          ffn.gated_backward_bound(dh, GEMM_REL * s, zz, **act), "dz")
+            ref, s = oracle.gemm(w["a"][0][o:o + n], w["a"][1][o:o + n], w["ws"][g][0], w["ws"][g][1], K)
+            assert_within(f64(h[o:o + n, :I]), ffn.gated(ref, **act), ffn.gated_bound(ref, GEMM_REL * s, **act), "h")
+            assert_within(f64(zo[o:o + n, :2 * I]), ref, ffn.BF16_HALF * (np.abs(ref) + GEMM_REL * s) + GEMM_REL * s + ffn.FLOOR, "z")
+    for t, n in ((out, 2 * I), (h, I), (zo, 2 * I)):
+        assert torch.all(t[~written] == 9) and torch.all(t[:, n:] == 9)
+    before = z.clone()
+    mx.mxfp4_grouped_gated_gemm_backward(*args, **act, out=z[:, :2 * I])
+    assert torch.equal(z[written, :2 * I], out[written, :2 * I])
+    assert torch.equal(z[~written], before[~written]) and torch.equal(z[:, 2 * I:], before[:, 2 * I:])
