@@ -244,3 +244,20 @@ def test_grouped_gated_odd_columns(sizes, I, K):
     mx.mxfp4_grouped_gated_gemm_backward(*args, **act, out=z[:, :2 * I])
     assert torch.equal(z[written, :2 * I], out[written, :2 * I])
     assert torch.equal(z[~written], before[~written]) and torch.equal(z[:, 2 * I:], before[:, 2 * I:])
+
+
+# ------------------------------------------------------------------ dropout's counter
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("first", [2 ** 32 - 1000, 2 ** 32 - 100_000_000, 2 ** 32, 3 * 2 ** 32 + 12345])
+def test_dropout_block_numbers_past_32_bits(first, dtype):
+    """A large tensor whose Philox blocks (four elements each) start before 2^32 and
+    run past it inside the launch, and ones that lie behind it: rows on both sides
+    draw the words of their 64-bit number."""
+    rows, cols = 150_000, 4096                                  # 153.6 M blocks
+    x = torch.ones((rows, cols), dtype=dtype, device="cuda")
+    y = mx.mxfp4_dropout(x, 0.5, 5, 4 * first)
+    cross = (2 ** 32 - first) * 4 // cols
+    at = {0, 1, 2, 3, rows // 2, rows - 1} | {r for r in range(cross - 2, cross + 3) if 0 <= r < rows}
+    for r in sorted(at):
+        want = ffn.dropout_words(cols, 5, 4 * first + r * cols) >= (1 << 31)
+        assert np.array_equal(y[r].float().cpu().numpy() == 2, want), r
