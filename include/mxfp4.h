@@ -265,7 +265,8 @@ MXFP4_API int mxfp4_dequantize(const uint8_t *codes, int64_t ld_codes,
  *
  * a_codes [M, K/2] (row stride lda bytes), a_scales MMA layout for (M x K);
  * b_codes [N, K/2] (ldb), b_scales MMA layout for (N x K); c [M, N] FP32
- * (row stride ldc elements), fully overwritten.  A 2D-quantized weight is
+ * (row stride ldc elements), fully overwritten; columns past N in wider rows are
+ * left as they were (here and in every other product).  A 2D-quantized weight is
  * used as B through its codes (fprop) or its transposed copy (dgrad) with the
  * matching MMA scales.
  *

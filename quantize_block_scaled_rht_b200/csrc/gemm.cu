@@ -64,8 +64,13 @@ constexpr int MAX_STAGES = 8;
 // its column steps in turn.
 // SUB: if not 0, the tiles of the last, partial round are cut into pieces of SUB
 // columns (get_item).
+// RAGGED: dense FP32 and bf16 outputs whose columns end inside 16 bytes
+// (ragged_box).  A form of its own: the test, even once per tile, cost the bf16
+// product of 4096 x 5760 x 2880 2% (35.9 -> 36.6 us; grouped forms, which have both
+// ways of storing anyway, nothing).
 constexpr int KIND_MX = 0, KIND_NV = 1, KIND_I8 = 2;
-template <int BN_, int STAGES_, int KCH_, int KIND_ = KIND_MX, int EPI_BUFS_ = 2, int EPI_WARPS_ = 4, int SUB_ = 0>
+template <int BN_, int STAGES_, int KCH_, int KIND_ = KIND_MX, int EPI_BUFS_ = 2, int EPI_WARPS_ = 4, int SUB_ = 0,
+          bool RAGGED_ = false>
 struct TileCfg {
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
@@ -76,6 +81,7 @@ struct TileCfg {
     static constexpr int SPLIT = EPI_WARPS / 4;       // warps per lane quarter
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int SUB = SUB_;
+    static constexpr bool RAGGED = RAGGED_;
     static constexpr int PIECES = SUB ? BN / SUB : 1;
     static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * EPI_BUF;
     static constexpr int KPB = I8 ? 1 : 2;            // K-elements per byte
@@ -125,6 +131,8 @@ constexpr int OUT_F32 = 0, OUT_BF16 = 1, OUT_MX = 2, OUT_GATED = 3, OUT_GATED_BW
 
 using DefaultCfg = TileCfg<192, 3, 2>;
 using NvCfg = TileCfg<192, 5, 1, KIND_NV>;
+using RaggedCfg = TileCfg<192, 3, 2, KIND_MX, 2, 4, 0, true>;
+using RaggedNvCfg = TileCfg<192, 5, 1, KIND_NV, 2, 4, 0, true>;
 // The gated epilogues take eight warps.  Forward: one staging buffer each, which
 // keeps the 3 x 512 ring (4096 x 5760 x 2880, h alone: 35.1 us, the bf16
 // product's time; 4 warps and two buffers 48.8, 8 warps and two buffers on a
@@ -184,6 +192,7 @@ struct GemmParams {
     const int32_t *group_sizes;
     const float *a_amax, *b_amax;   // NVFP4 tensor amaxes (second-level scales amax / 2688)
     const float *a_tok, *b_chan;    // int8: one scale per row of A, one per row of B (all groups')
+    int64_t box_n0;                 // FP32, bf16: last first column of a tile without a ragged box
     void *z;                        // gated: pre-activations out (may be null); backward: in
     int64_t ldz;
     float act_alpha, act_limit, act_beta;
@@ -795,7 +804,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             // one answer for the warp: what follows needs it whole
             if (!__all_sync(0xFFFFFFFFu, wait_phase(&sh->tmem_full[acc], acc_ph, sh, limit))) break;
             tc_fence_after();
-            const bool full_box = MODE == MODE_DENSE || (row_lo + 32 <= ti.rows_valid);
+            bool full_box = MODE == MODE_DENSE || (row_lo + 32 <= ti.rows_valid);
+            if constexpr (!Cfg::I8 && (OUT == OUT_F32 || OUT == OUT_BF16) && (MODE != MODE_DENSE || Cfg::RAGGED))
+                full_box = full_box && ti.n0 <= p.box_n0;
             const bool any_row = row_lo < ti.rows_valid;
             const bool empty_k = ti.kg <= 0;              // grouped K: an empty group's output is zero
             if constexpr (OUT == OUT_MX) {
@@ -1276,6 +1287,7 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     p.group_offsets = g.offsets; p.group_sizes = g.sizes; p.num_groups = g.G;
     p.a_amax = g.a_amax; p.b_amax = g.b_amax;
     p.a_tok = g.a_tok; p.b_chan = g.b_chan;
+    p.box_n0 = (g.N * (OUT == OUT_F32 ? 4 : 2)) % 16 ? g.N - BN : g.N;
     p.z = g.z; p.ldz = g.ldz;
     p.act_alpha = g.alpha; p.act_limit = g.limit; p.act_beta = g.beta;
     p.cut_whole = g.cut_whole; p.cut_tiles = g.cut_tiles; p.cut_last = g.cut_last; p.cut_items = g.cut_items;
@@ -1297,7 +1309,7 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
 int launch_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, const uint8_t *b_codes, int64_t ldb,
                 const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, float *c, int64_t ldc, cudaStream_t s) {
     GemmArgs g{a_codes, a_scales, b_codes, b_scales, lda, ldb, M, N, K, ldc, c, nullptr, nullptr, 1};
-    return launch_cfg<DefaultCfg, MODE_DENSE>(g, s);
+    return N % 4 ? launch_cfg<RaggedCfg, MODE_DENSE>(g, s) : launch_cfg<DefaultCfg, MODE_DENSE>(g, s);
 }
 
 int launch_grouped_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, int64_t a_rows,
@@ -1311,7 +1323,7 @@ int launch_gemm_bf16(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scale
                      int64_t ldb, const uint8_t *b_scales, int64_t M, int64_t N, int64_t K, uint16_t *c, int64_t ldc,
                      cudaStream_t s) {
     GemmArgs g{a_codes, a_scales, b_codes, b_scales, lda, ldb, M, N, K, ldc, c, nullptr, nullptr, 1};
-    return launch_cfg<DefaultCfg, MODE_DENSE, OUT_BF16>(g, s);
+    return N % 8 ? launch_cfg<RaggedCfg, MODE_DENSE, OUT_BF16>(g, s) : launch_cfg<DefaultCfg, MODE_DENSE, OUT_BF16>(g, s);
 }
 
 int launch_grouped_gemm_bf16(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scales, int64_t a_rows,
@@ -1350,7 +1362,7 @@ int launch_nvfp4_gemm(const uint8_t *a_codes, int64_t lda, const uint8_t *a_scal
                       const uint8_t *b_codes, int64_t ldb, const uint8_t *b_scales, const float *b_amax, int64_t M,
                       int64_t N, int64_t K, float *c, int64_t ldc, cudaStream_t s) {
     GemmArgs g{a_codes, a_scales, b_codes, b_scales, lda, ldb, M, N, K, ldc, c, nullptr, nullptr, 1, a_amax, b_amax};
-    return launch_cfg<NvCfg, MODE_DENSE>(g, s);
+    return N % 4 ? launch_cfg<RaggedNvCfg, MODE_DENSE>(g, s) : launch_cfg<NvCfg, MODE_DENSE>(g, s);
 }
 
 // Launch with the last round of tiles cut into pieces where those fit one round.
