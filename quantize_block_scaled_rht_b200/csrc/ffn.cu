@@ -24,9 +24,10 @@ __device__ __forceinline__ void st_v2(void *p, uint32_t a, uint32_t b) {
 
 // ---------------------------------------------------------------------------
 // int8 token quantizer: per row a = max(amax, 2^-100), scale = a / 127, codes
-// RNE(x * i) with i = 127 * (1 / a), each step rounded to FP32 (i is within 1.5
-// steps of 2^-24 of 127 / a, so |x i| stays below 127.5).  The floor keeps 1 / a
-// finite; a NaN or Inf anywhere in the row gives the scale NaN and codes 0.
+// RNE(x * i) with i = 127 * (1 / a), each step rounded to FP32 (i is within 1.5 x
+// 2^-24 of 127 / a, relative, and for a > 2^126, where 1 / a is subnormal, within
+// 4.1 x 2^-24: |x i| stays below 127.001).  The floor keeps 1 / a finite; a NaN or
+// Inf anywhere in the row gives the scale NaN and codes 0.
 //
 // Bound by HBM (2 B read, 1 B written per element; 16384 x 11520: 81 us, 7.0 TB/s
 // with part of the writes still in L2).  T threads hold one row in registers (V

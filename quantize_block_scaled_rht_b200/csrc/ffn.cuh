@@ -21,9 +21,10 @@ struct GatedAct {
     float alpha, limit, beta;
 
     // s = 1 / (1 + 2^(-alpha log2(e) g)) of N values with the hardware's base-2
-    // exponential and reciprocal: the product's rounding moves the exponent by
-    // at most |alpha g| 2^-23, which for the |g| where s is not yet 0 or 1 leaves
-    // a relative error under 1e-5, a hundredth of bf16's half-step.  Both flush
+    // exponential and reciprocal: the roundings of log2(e), of its product with
+    // alpha and of that with g move the exponent by at most 1.1 x 2^-23 |alpha g|,
+    // which leaves a relative error under 1e-5 for |alpha g| < 60 and under 2e-5 up
+    // to where s is 0 or 1, a two-hundredth of bf16's half-step.  Both flush
     // subnormals (an exponential below 2^-126 leaves s = 1, a sum above 2^126
     // s = 0); the forms that keep them cost a branch each.  One step for all N
     // values at a time: a warp of the GEMM's epilogue has a scheduler to itself,
@@ -128,7 +129,7 @@ struct Int8Args {
 // with K (a first round of tiles: about (5000 + K) * 0.9 ns) until N fills the
 // device, and hardly with the rows.  The limits are where the two times meet (41
 // sizes, N 256 to 178560, K 256 to 8192, weights in L2 and from HBM): by these
-// rules no size is more than 6% (gated) or 5% (int8) off the faster kernel, where
+// rules no size is more than 7% (gated) or 3% (int8) off the faster kernel, where
 // all calls of up to four rows by the streaming kernel were up to 2.9 and 1.7
 // times slower (4 rows of 178560 x 2880: gated 199 us against 68, int8 156
 // against 94).  One int8 row streams B as fast as the tile kernel at any size

@@ -137,9 +137,9 @@ using RaggedNvCfg = TileCfg<192, 5, 1, KIND_NV, 2, 4, 0, true>;
 // keeps the 3 x 512 ring (4096 x 5760 x 2880, h alone: 35.1 us, the bf16
 // product's time; 4 warps and two buffers 48.8, 8 warps and two buffers on a
 // ring of 5 x 256 40.2).  Backward: two buffers carry z in and dz out, beside a
-// ring of 5 x 256 (4096 x 2880 x 2880 37.0 us, K = 5760 50.8; three buffers and a
-// ring of 4 x 256 37.0 and 54.2, four of 3 x 256 41.7 and 61.6, 4 warps 43.3, 12
-// warps 41.2).
+// ring of 5 x 256 (when chosen, with whole last rounds, 4096 x 2880 x 2880 37.0 us,
+// K = 5760 50.8; three buffers and a ring of 4 x 256 37.0 and 54.2, four of 3 x 256
+// 41.7 and 61.6, 4 warps 43.3, 12 warps 41.2).
 using GatedCfg = TileCfg<192, 3, 2, KIND_MX, 1, 8>;
 using BwdCfg = TileCfg<192, 5, 1, KIND_MX, 2, 8>;
 // Calls take 128-column tiles where those finish in clearly fewer rounds of
@@ -150,25 +150,25 @@ using BwdNarrowCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8>;
 // The backward epilogue outlasts the MMAs, so a last round that only a few pairs
 // take part in costs a whole tile's epilogue.  A dense call whose last round
 // still fits one round in 64-column pieces takes the form that cuts it (launch_cut):
-// 4096 x 2880 x 2880 34.6 against 36.9 us (K = 64: 26.2 against 29.1), 16 rows
-// 9.2 against 10.4, 1024 x 1024 x 1024 7.3 against 8.6.  The counting costs calls
+// 4096 x 2880 x 2880 34.1 against 38.4 us (K = 64: 25.7 against 30.4), 16 rows
+// 9.6 against 10.9, 1024 x 1024 x 1024 7.6 against 9.1.  The counting costs calls
 // that cut nothing 1 to 3%, so they, and the grouped calls, whose number of tiles
 // the host does not know, have the plain form.
 using BwdCutCfg = TileCfg<192, 5, 1, KIND_MX, 2, 8, 64>;
 using BwdNarrowCutCfg = TileCfg<128, 6, 1, KIND_MX, 2, 8, 64>;
 // int8: without scale factors in tensor memory two 256-column accumulators fit,
 // and a 256 x 256 tile reads 1/8 fewer operand bytes per product than 256 x 192
-// (4096 x 2880 x 2880: 28.6 us, 256 x 192 33.8, and 31.7 with the ring as 3 x 256
-// instead of 6 x 128 K-elements).
+// (4096 x 2880 x 2880 with a whole last round: 27.3 us, 256 x 192 30.4, and 28.8
+// with the ring as 3 x 256 instead of 6 x 128 K-elements).
 // Narrow: 128 x 2880 x 2880 10.2 against 12.6 us, 64 x 8192 x 8192 19.8 against
 // 24.4; where it would take two rounds to the wide tile's one, the fewer operand
 // bytes win (1024 x 2880 x 2880: 13.8 against 16.4).
 using I8Cfg = TileCfg<256, 6, 1, KIND_I8>;
 using I8NarrowCfg = TileCfg<128, 8, 1, KIND_I8>;
 // The last round of a dense call in 128-column pieces, with B boxes of their
-// size, where those fit one round: 2048 x 2880 x 2880 18.4 against 19.8 us (96
+// size, where those fit one round: 2048 x 2880 x 2880 18.5 against 20.1 us (96
 // tiles: a round of 74, then 14 tiles in two pieces and 8 of the last 64 columns in
-// one), 1024 x 5760 x 2880 18.2 against 19.5, 4096 x 2880 x 2880 25.7 against 27.2.
+// one), 1024 x 5760 x 2880 18.6 against 20.2, 4096 x 2880 x 2880 26.1 against 27.3.
 // Narrow tiles in 64-column pieces: 512 x 1024 x 1024 6.3 against 6.6, but 16 x
 // 2880 x 2880 9.85 against 9.5; not kept.
 using I8CutCfg = TileCfg<256, 6, 1, KIND_I8, 2, 4, 128>;
