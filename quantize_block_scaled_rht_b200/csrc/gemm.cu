@@ -65,9 +65,12 @@ constexpr int MAX_STAGES = 8;
 // SUB: if not 0, the tiles of the last, partial round are cut into pieces of SUB
 // columns (get_item).
 // RAGGED: dense FP32 and bf16 outputs whose columns end inside 16 bytes
-// (ragged_box).  A form of its own: the test, even once per tile, cost the bf16
-// product of 4096 x 5760 x 2880 2% (35.9 -> 36.6 us; grouped forms, which have both
-// ways of storing anyway, nothing).
+// (ragged_box).  The output's tensor map ends at the last whole 16 bytes, and the
+// columns behind go out with plain stores (4096 x 190 x 2880 bf16 8.8 us; the whole
+// last box that way 9.6, the whole last tile 10.1).  A form of its own: the test,
+// even once per tile, cost the bf16 product of 4096 x 5760 x 2880 2% (35.9 -> 36.6
+// us; grouped forms, which have both ways of storing anyway, nothing: they store the
+// last column of tiles plainly).
 constexpr int KIND_MX = 0, KIND_NV = 1, KIND_I8 = 2;
 template <int BN_, int STAGES_, int KCH_, int KIND_ = KIND_MX, int EPI_BUFS_ = 2, int EPI_WARPS_ = 4, int SUB_ = 0,
           bool RAGGED_ = false>
@@ -192,7 +195,8 @@ struct GemmParams {
     const int32_t *group_sizes;
     const float *a_amax, *b_amax;   // NVFP4 tensor amaxes (second-level scales amax / 2688)
     const float *a_tok, *b_chan;    // int8: one scale per row of A, one per row of B (all groups')
-    int64_t box_n0;                 // FP32, bf16: last first column of a tile without a ragged box
+    int64_t box_n0;                 // grouped FP32, bf16: last first column of a tile without a ragged box
+    int64_t box_cols;               // RAGGED: columns up to the last whole 16 bytes
     void *z;                        // gated: pre-activations out (may be null); backward: in
     int64_t ldz;
     float act_alpha, act_limit, act_beta;
@@ -805,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             if (!__all_sync(0xFFFFFFFFu, wait_phase(&sh->tmem_full[acc], acc_ph, sh, limit))) break;
             tc_fence_after();
             bool full_box = MODE == MODE_DENSE || (row_lo + 32 <= ti.rows_valid);
-            if constexpr (!Cfg::I8 && (OUT == OUT_F32 || OUT == OUT_BF16) && (MODE != MODE_DENSE || Cfg::RAGGED))
+            if constexpr (!Cfg::I8 && (OUT == OUT_F32 || OUT == OUT_BF16) && MODE != MODE_DENSE)
                 full_box = full_box && ti.n0 <= p.box_n0;
             const bool any_row = row_lo < ti.rows_valid;
             const bool empty_k = ti.kg <= 0;              // grouped K: an empty group's output is zero
@@ -1010,11 +1014,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (lane == 0 && (!Cfg::RAGGED || col0 < p.box_cols)) {
                             tma_store_2d(&tma_c, (int32_t)col0, (int32_t)(ti.c_row0 + row_lo), buf);
                             bulk_commit_group();
                         }
                         ++buf_i;
+                        if (Cfg::RAGGED && col0 + 64 > p.box_cols && row_lo + lane < ti.rows_valid) {
+                            uint16_t *dst = static_cast<uint16_t *>(p.c) + (ti.c_row0 + row_lo + lane) * p.ldc + p.box_cols;
+                            const int left = (int)(p.N - p.box_cols);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                if (col0 + 8 * c != p.box_cols) continue;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if (2 * e + 2 <= left) *reinterpret_cast<uint32_t *>(dst + 2 * e) = w[4 * c + e];
+                                    else if (2 * e < left) dst[2 * e] = (uint16_t)w[4 * c + e];
+                                }
+                            }
+                        }
                     } else if (row_lo + lane < ti.rows_valid) {
                         uint16_t *dst = static_cast<uint16_t *>(p.c) + (ti.c_row0 + row_lo + lane) * p.ldc + col0;
 #pragma unroll
@@ -1068,11 +1085,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (lane == 0 && (!Cfg::RAGGED || col0 < p.box_cols)) {
                             tma_store_2d(&tma_c, (int32_t)col0, (int32_t)(ti.c_row0 + row_lo), buf);
                             bulk_commit_group();
                         }
                         ++buf_i;
+                        if (Cfg::RAGGED && col0 + 32 > p.box_cols && row_lo + lane < ti.rows_valid) {
+                            float *dst = static_cast<float *>(p.c) + (ti.c_row0 + row_lo + lane) * p.ldc + p.box_cols;
+                            const int left = (int)(p.N - p.box_cols);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                if (col0 + 4 * c != p.box_cols) continue;
+#pragma unroll
+                                for (int e = 0; e < 3; ++e)
+                                    if (e < left) dst[e] = __uint_as_float(v[4 * c + e]);
+                            }
+                        }
                     } else if (row_lo + lane < ti.rows_valid) {
                         float *dst = static_cast<float *>(p.c) + (ti.c_row0 + row_lo + lane) * p.ldc + col0;
     #pragma unroll
@@ -1246,6 +1274,9 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     constexpr CUtensorMapDataType BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     constexpr CUtensorMapSwizzle SW128 = CU_TENSOR_MAP_SWIZZLE_128B;
     const uint64_t kbytes = (uint64_t)(g.K / Cfg::KPB), N = (uint64_t)g.N, ldc = (uint64_t)g.ldc;
+    constexpr int64_t per16 = OUT == OUT_F32 ? 4 : 8;
+    // (a map has at least one column; where there are none to store it is not used)
+    const uint64_t c_cols = !Cfg::RAGGED ? N : (uint64_t)(g.N < per16 ? per16 : g.N / per16 * per16);
     bool ok = make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a_codes, kbytes, (uint64_t)g.M, (uint64_t)g.lda, CHUNK, a_box,
                        SW128) &&
               make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b_codes, kbytes, (uint64_t)G * N, (uint64_t)g.ldb, CHUNK,
@@ -1258,9 +1289,9 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     else if constexpr (OUT == OUT_GATED_BWD)
         ok = ok && make_map(&tc, BF, g.c, 2 * N, (uint64_t)c_rows, ldc * 2, 64, 32, SW128);
     else if constexpr (OUT == OUT_BF16)
-        ok = ok && make_map(&tc, BF, g.c, N, (uint64_t)c_rows, ldc * 2, 64, 32, SW128);
+        ok = ok && make_map(&tc, BF, g.c, c_cols, (uint64_t)c_rows, ldc * 2, 64, 32, SW128);
     else
-        ok = ok && make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.c, N, (uint64_t)c_rows, ldc * 4, 32, 32, SW128);
+        ok = ok && make_map(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.c, c_cols, (uint64_t)c_rows, ldc * 4, 32, 32, SW128);
     if (!ok) return MXFP4_ERR_CUDA;
     tz = tsa = tsb = tc;                       // never used where an operand below does not exist
     if ((OUT == OUT_GATED || OUT == OUT_GATED_BWD) && g.z &&
@@ -1287,7 +1318,8 @@ static int launch_cfg(const GemmArgs &g, cudaStream_t s) {
     p.group_offsets = g.offsets; p.group_sizes = g.sizes; p.num_groups = g.G;
     p.a_amax = g.a_amax; p.b_amax = g.b_amax;
     p.a_tok = g.a_tok; p.b_chan = g.b_chan;
-    p.box_n0 = (g.N * (OUT == OUT_F32 ? 4 : 2)) % 16 ? g.N - BN : g.N;
+    p.box_n0 = g.N % per16 ? g.N - BN : g.N;
+    p.box_cols = g.N / per16 * per16;
     p.z = g.z; p.ldz = g.ldz;
     p.act_alpha = g.alpha; p.act_limit = g.limit; p.act_beta = g.beta;
     p.cut_whole = g.cut_whole; p.cut_tiles = g.cut_tiles; p.cut_last = g.cut_last; p.cut_items = g.cut_items;

@@ -35,6 +35,23 @@ def test_dense(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M", [30, 300])
+def test_every_remainder(M, dtype):
+    """Last columns at every place of a box and of 16 bytes: the columns of a wider product, bit for bit."""
+    N, K = 216, 128
+    ca, sa = base._oracle_operand(synth.normal_bf16((M, K), 1))
+    cb, sb = base._oracle_operand(synth.normal_bf16((N, K), 2, 0.1))
+    a, b, s = (dev_u8(ca), dev_u8(to_mma(sa, K))), dev_u8(cb), dev_u8(to_mma(sb, K))
+    fn = mx.mxfp4_gemm if dtype == torch.float32 else mx.mxfp4_gemm_bf16
+    whole = fn(*a, b, s, K)
+    for n in [*range(1, 74), *range(121, 138), *range(185, 217)]:
+        buf, out = _wide(M, n, dtype)
+        fn(*a, b[:n], s, K, out=out)
+        assert torch.equal(out, whole[:, :n]) and torch.all(buf[:, n:] == 5), n
+    assert mx.mxfp4_get_error() == mx.MXFP4_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("sizes,N,K", [([1, 130, 0, 257, 128], 195, 256), ([300, 5, 64], 390, 576)])
 def test_grouped(sizes, N, K, dtype):
     sizes, offsets, rows, a, _ = base._grouped_case(sizes, N, K)
