@@ -87,11 +87,12 @@ struct GatedAct {
             const uint32_t z0 = z[2 * i], z1 = z[2 * i + 1];
             const float2 u = make_float2(clamp_up(bf16hi(z0)), clamp_up(bf16hi(z1)));
             const float2 d = make_float2(__uint_as_float(dh[2 * i]), __uint_as_float(dh[2 * i + 1]));
-            // dh s (1 + alpha g (1 - s)) as dh s + alpha (dh g s (1 - s)): alpha g may
-            // leave FP32's range for finite g, and as an infinity would meet a zero s
-            // or 1 - s; dh g s is du itself
+            // dh s (1 + alpha g (1 - s)) as hs + alpha (hs (g (1 - s))), hs = dh s: alpha g
+            // and du = dh g s may leave FP32's range for finite g, and as infinities would
+            // meet a zero s or 1 - s.  (With du (1 - s) in the middle, one product less, du's
+            // overflow made dg NaN.)
             const float2 hs = mul2(d, s[i]), du = mul2(hs, g[i]);
-            const float2 dg = mul2(fma2(a, mul2(du, sub2(one, s[i])), hs), add2(u, b));
+            const float2 dg = mul2(fma2(a, mul2(hs, mul2(g[i], sub2(one, s[i]))), hs), add2(u, b));
             // beyond the limit 0, and NaN where zu is
             const float2 o = sub2(u, u);
             z[2 * i] = pack_bf16x2(bf16lo(z0) > limit ? 0.0f : dg.x, fabsf(bf16hi(z0)) <= limit ? du.x : o.x);

@@ -52,6 +52,31 @@ def test_gated_backward_of_gates_near_the_largest_finite_value(M, act):
         assert_within(dz[:, 1::2][above], want[:, 1::2][above], bound[:, 1::2][above], "dz up")
 
 
+@pytest.mark.parametrize("act", [ffn.SWIGLU, NO_LIMIT])
+@pytest.mark.parametrize("M", [3, 150])
+def test_gated_backward_where_the_up_gradient_overflows(M, act):
+    """dh g beyond the largest finite value is an infinity in the up value's gradient
+    and nothing else: the gate's is dh (u + beta), or 0 where s is."""
+    I, K = 72, 128
+    ca, sa, da, dsa = operand(M, K, 3, 1e3)
+    cb, sb, db, dsb = operand(I, K, 4, 10.0)
+    z = np.random.default_rng(5).standard_normal((M, 2 * I)).astype(np.float32)
+    z[:, 0::2] = np.array([-3.3e38, -2.9e38, 2.9e38, 3.3e38], np.float32)[np.arange(M * I).reshape(M, I) % 4]
+    zb = synth.bf16_bits(z)
+    dz = f64(mx.mxfp4_gated_gemm_backward(da, dsa, db, dsb, dev_bf16(zb), K, **act))
+    no_error()
+    dh, s = oracle.gemm(ca, sa, cb, sb, K)
+    z64 = synth.bf16_to_f32(zb).astype(np.float64)
+    below, above = z64[:, 0::2] < 0, z64[:, 0::2] > 0
+    assert np.all(dz[:, 0::2][below] == 0) and np.all(dz[:, 1::2][below] == 0)
+    far = above & (np.abs(dh) > 10 + GEMM_REL * s)
+    assert far.sum() > 0.4 * far.size and np.array_equal(dz[:, 1::2][far], np.copysign(np.inf, dh[far]))
+    u = z64[:, 1::2] + act["beta"]
+    want = dh * u
+    slack = GEMM_REL * s * np.abs(u) + 3 * 2.0 ** -24 * np.abs(want)
+    assert_within(dz[:, 0::2][above], want[above], (ffn.BF16_HALF * (np.abs(want) + slack) + slack + ffn.FLOOR)[above], "dz gate")
+
+
 @pytest.mark.parametrize("act", [ffn.SWIGLU, ffn.CLAMPED])
 @pytest.mark.parametrize("M", [3, 150])
 def test_gated_backward_nan_pre_activations(M, act):
